@@ -28,10 +28,12 @@
  *     stream) and runs asynchronously.  Argument errors are detected on the
  *     host and returned before anything is launched.
  *   - Query row i of batch b sits at absolute position t = q_offset + i and
- *     sees key positions s <= t.  Requirement: q_offset + Lq <= Lk.
+ *     sees key positions s <= t.  Requirement: q_offset + Lq <= Lk (the
+ *     KV-cache entry points say where they differ).
  *     Prefill: q_offset = 0, Lq = Lk.  Decode: Lq = 1, q_offset = Lk - 1.
  *   - Supported shapes: d_I in {64, 128}; H_I a power of two in [4, 128];
- *     d in {64, 128}; Hq in {8, 16}; Hkv == 1 (MQA); 1 <= k <= Lk.  Other
+ *     d in {64, 128}; Hq in {8, 16}; Hkv == 1 (MQA; ic_prefix_attn and
+ *     ic_attn_mass take more); 1 <= k <= Lk.  Other
  *     shapes return IC_ERR_UNSUPPORTED.  Alignment:
  *       - bf16 buffers, the indexer's head weights w and every workspace
  *         must be 16-byte aligned: kernels read them with 16-byte vector,
@@ -74,7 +76,8 @@ const char *ic_last_error_message(void);
 
 /* Synchronises `stream`, reads and clears the current device's error word.
  * Returns IC_OK, IC_ERR_TIMEOUT (a bounded wait expired) or
- * IC_ERR_INVALID_ARG (an attention index outside [0, t] was skipped), or
+ * IC_ERR_INVALID_ARG (an attention index outside [0, t] was skipped, or a
+ * sequence length outside its cache was clamped), or
  * IC_ERR_CUDA if the synchronisation itself failed. */
 int ic_get_last_device_error(ic_stream_t stream);
 
@@ -352,6 +355,113 @@ int ic_layer_stack_fused_fallback_blocks(const ic_dims *dims, const ic_stack_opt
  */
 int ic_index_overlap(const int32_t *idx_a, const int32_t *idx_b, long long n_rows, int k, int Lk,
                      int32_t *counts, ic_stream_t stream);
+
+/*
+ * Attention of a batch whose sequences share one prefix (a common system
+ * prompt, a document, the prompt of many rollouts): the prefix keys are read
+ * once for all query rows instead of once per sequence.
+ *   q [B, Lq, Hq, d] bf16
+ *   k_prefix, v_prefix [P, Hkv, d] bf16    shared by every sequence (P >= 0)
+ *   k, v [B, S, Hkv, d] bf16               each sequence's own cache of S rows
+ *                                          (S >= 0; NULL when S == 0)
+ *   lens [B] int32 (device; NULL: every sequence holds S positions)
+ *   out [B, Lq, Hq, d] bf16 (written)      lse [B, Lq, Hq] fp32 (written; may be NULL)
+ * lens[b] counts the own positions of sequence b, the Lq query tokens' own
+ * among them.  Row i of sequence b attends over all P prefix keys and the own
+ * positions s <= lens[b] - Lq + i (none when that is negative):
+ *   z = scale * q . K,  out = sum softmax(z) * V,  lse = ln sum e^z.
+ * A row that sees nothing gives out = 0, lse = -INFINITY.  Own rows at or past
+ * lens[b] may hold anything.  Own rows s < lens[b] must be finite: a row of V
+ * that is not makes every row of its sequence non-finite, also those that do
+ * not see it.  A length outside [0, S] is clamped and flags
+ * IC_ERR_INVALID_ARG in the device error word.  d in {64, 128}; Hq <= 128 a
+ * multiple of Hkv, query head h reads K/V head h / (Hq / Hkv).  scale <= 0
+ * selects 1/sqrt(d).
+ * ws/ws_bytes: device workspace of ic_prefix_attn_workspace_bytes(...) bytes
+ * for the partial results of rows whose keys are split over several CTAs;
+ * with less (ws may be NULL when ws_bytes is 0) keys are split less or not at
+ * all, and results differ only by the rounding of the merges.
+ */
+int ic_prefix_attn(const uint16_t *q, const uint16_t *k_prefix, const uint16_t *v_prefix,
+                   const uint16_t *k, const uint16_t *v, const int32_t *lens, int B, int Lq, int P,
+                   int S, int Hq, int Hkv, int d, float scale, uint16_t *out, float *lse, void *ws,
+                   size_t ws_bytes, ic_stream_t stream);
+
+/* Workspace with which ic_prefix_attn splits keys as it prefers (0 for
+ * invalid sizes). */
+size_t ic_prefix_attn_workspace_bytes(int B, int Lq, int P, int S, int Hq, int Hkv, int d);
+
+/*
+ * The attention weight each cached position received, added to a running
+ * total (what an eviction policy ranks positions by):
+ *   q [B, Lq, Hq, d] bf16   k [B, Lk, Hkv, d] bf16   lse [B, Lq, Hq] fp32
+ *   lens [B] int32 (device; may be NULL)   mass [B, Lk] fp32 (added to)
+ *   mass[b,s] += sum over rows i that see s and heads h of exp(scale q.k[s] - lse[b,i,h])
+ * lse is the natural-log normaliser that an attention call returned for the
+ * row (over these keys, or over these and others: the prefix and the own cache of
+ * ic_prefix_attn each get their share).  Row i of sequence b sees positions
+ * s <= t: t = lens[b] - Lq + i and s < lens[b] with lens, else t = q_offset + i
+ * (q_offset + Lq may exceed Lk here: q_offset >= Lk lets every row see every
+ * key, as the rows of a batch see a shared prefix).  Rows with
+ * lse = -INFINITY add nothing.  Positions that no row sees keep their value,
+ * and their keys may hold anything.  Shapes as in ic_prefix_attn.  The sum has a fixed order:
+ * the same call gives the same bits.
+ */
+int ic_attn_mass(const uint16_t *q, const uint16_t *k, const float *lse, const int32_t *lens, int B,
+                 int Lq, int Lk, int Hq, int Hkv, int d, int q_offset, float scale, float *mass,
+                 ic_stream_t stream);
+
+/*
+ * ic_attn_mass over the slots of an index cache: every slot of idx
+ * [B, Lq, k_slots] adds its weight to the position it names (a position
+ * repeated in a row counts every time, as in ic_sparse_attn, whose lse this
+ * takes).  Slots holding -1 are empty; a slot outside [0, t] is skipped and
+ * flags IC_ERR_INVALID_ARG in the device error word.  Shapes as in
+ * ic_sparse_attn (Hkv == 1, Hq 8 or 16).
+ * With Lq > 1 several rows add to one position: their weights are summed as
+ * 64-bit fixed point in ws (ic_attn_mass_sparse_workspace_bytes(...) bytes,
+ * cleared by the call), whose result does not depend on the order, so the same
+ * call gives the same bits.  A sum with a weight that is NaN or above 2 Hq
+ * (lse not the row's) comes out NaN.
+ */
+int ic_attn_mass_sparse(const uint16_t *q, const uint16_t *k, const int32_t *idx, const float *lse,
+                        int B, int Lq, int Lk, int Hq, int Hkv, int d, int k_slots, int q_offset,
+                        float scale, float *mass, void *ws, size_t ws_bytes, ic_stream_t stream);
+
+/* Workspace ic_attn_mass_sparse needs (0 when Lq <= 1). */
+size_t ic_attn_mass_sparse_workspace_bytes(int B, int Lq, int Lk);
+
+/*
+ * The positions a cache keeps under a budget of n_keep:
+ *   mass [B, Lk] fp32   lens [B] int32 (device; NULL: Lk)
+ *   keep [B, n_keep] int32 (written)   new_lens [B] int32 (written; may be NULL)
+ * A sequence of n = lens[b] positions keeps min(n, n_keep): all of them when
+ * n <= n_keep, else its first n_sink, its last n_recent and, of the others,
+ * those first in the order (mass descending, position ascending; NaN ranks as
+ * -INFINITY).  Positions are written ascending, then -1.  new_lens[b] =
+ * min(n, n_keep).  n_sink + n_recent <= n_keep.  A length outside [0, Lk] is
+ * clamped and flags IC_ERR_INVALID_ARG in the device error word.  B <= 65535.  Exact.
+ */
+int ic_evict_select(const float *mass, const int32_t *lens, int B, int Lk, int n_keep, int n_sink,
+                    int n_recent, int32_t *keep, int32_t *new_lens, ic_stream_t stream);
+
+/* One tensor of ic_cache_gather. */
+typedef struct {
+    const void *src;        /* [B, Lk, row_bytes] */
+    void *dst;              /* [B, Lk_dst, row_bytes], overlapping nothing else of the call */
+    long long row_bytes;    /* a multiple of 4 up to 16 MiB */
+} ic_cache_copy;
+
+/*
+ * Compaction: dst[b, j] = src[b, keep[b, j]] for every tensor (up to 8: K, V,
+ * indexer keys, mass, ...) and every slot j of keep [B, n_keep] int32 that is
+ * not -1.  Rows of dst whose slot is -1, and rows at or past n_keep, are left as they
+ * were.  A slot outside [-1, Lk) is skipped and flags IC_ERR_INVALID_ARG in
+ * the device error word.  src and dst 4-byte aligned (16-byte aligned rows of
+ * a multiple of 16 bytes move in 16-byte accesses).
+ */
+int ic_cache_gather(const int32_t *keep, int B, int Lk, int n_keep, int Lk_dst, int n_tensors,
+                    const ic_cache_copy *copies, ic_stream_t stream);
 
 /*
  * Kernel launches this library has issued in this process so far (every

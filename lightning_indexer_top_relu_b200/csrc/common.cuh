@@ -18,6 +18,7 @@ enum : unsigned int {
     DEV_ERR_TIMEOUT = 1u,     // a bounded wait gave up
     DEV_ERR_BAD_INDEX = 2u,   // an attention index outside [0, t] (skipped)
     DEV_ERR_SMEM = 4u,        // the 1024-aligned shared-memory layout did not fit (kernel skipped)
+    DEV_ERR_BAD_LENGTH = 8u,  // a sequence length outside [0, capacity] (clamped)
 };
 
 constexpr int MAX_DYN_SMEM = 232448;          // 227 KB opt-in per CTA on sm_100

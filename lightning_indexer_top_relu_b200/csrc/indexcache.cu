@@ -17,11 +17,14 @@
 #include <mutex>
 
 #include "indexcache.h"
+#include "attn_mass.cuh"
+#include "cache_evict.cuh"
 #include "common.cuh"
 #include "dense_attn.cuh"
 #include "fused_topk.cuh"
 #include "index_overlap.cuh"
 #include "indexer_scores.cuh"
+#include "prefix_attn.cuh"
 #include "sparse_attn.cuh"
 #include "topk_select.cuh"
 
@@ -801,6 +804,8 @@ int device_setup(int* dev_out, int* sms_out) {
                              cudaFuncAttributeMaxDynamicSharedMemorySize, ic::SaSmem<64>::BYTES);
         cudaFuncSetAttribute(ic::sparse_attn_kernel<128>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, ic::SaSmem<128>::BYTES);
+        cudaFuncSetAttribute(ic::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ic::EvictSmem::bytes(ic::EV_CACHE_MAX));
         e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
         g_attn_cluster[dev] = attn_cluster_fits<64>() && attn_cluster_fits<128>();
@@ -903,6 +908,8 @@ int ic_get_last_device_error(ic_stream_t stream) {
         return fail(IC_ERR_CUDA, "a kernel's aligned shared-memory layout did not fit; it did no work");
     if (v & ic::DEV_ERR_BAD_INDEX)
         return fail(IC_ERR_INVALID_ARG, "an attention index outside [0, t] was skipped");
+    if (v & ic::DEV_ERR_BAD_LENGTH)
+        return fail(IC_ERR_INVALID_ARG, "a sequence length outside [0, capacity] was clamped");
     return IC_OK;
 }
 
@@ -1332,3 +1339,5 @@ int ic_layer_stack_fused_fallback_blocks(const ic_dims* dims, const ic_stack_opt
 }
 
 }  // extern "C"
+
+#include "cache_ops_abi.cuh"

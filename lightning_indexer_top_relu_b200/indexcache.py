@@ -36,7 +36,9 @@ EXPORTS = ("ic_status_string", "ic_last_error_message", "ic_get_last_device_erro
            "ic_sparse_attn_no_alloc", "ic_kernel_launch_count", "ic_sparse_attn_unique",
            "ic_sparse_attn_unique_workspace_bytes", "ic_index_overlap",
            "ic_layer_stack_dense_rows", "ic_layer_stack_forward_opts",
-           "ic_layer_stack_fused_fallback_blocks")
+           "ic_layer_stack_fused_fallback_blocks", "ic_prefix_attn",
+           "ic_prefix_attn_workspace_bytes", "ic_attn_mass", "ic_attn_mass_sparse",
+           "ic_attn_mass_sparse_workspace_bytes", "ic_evict_select", "ic_cache_gather")
 
 MARKS_PER_LAYER = 5        # IC_MARKS_PER_LAYER
 
@@ -71,6 +73,11 @@ class ICDims(ctypes.Structure):
                 ("q_offset", ctypes.c_int), ("H_I", ctypes.c_int), ("d_I", ctypes.c_int),
                 ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
                 ("k", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class ICCacheCopy(ctypes.Structure):
+    """ic_cache_copy: one tensor of a cache compaction."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("row_bytes", ctypes.c_longlong)]
 
 
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -121,6 +128,22 @@ _lib.ic_layer_stack_fused_fallback_blocks.argtypes = [ctypes.POINTER(ICDims),
 _lib.ic_layer_stack_forward.restype = _I
 _lib.ic_layer_stack_forward.argtypes = [ctypes.c_char_p, _I, ctypes.POINTER(ICLayer),
                                         ctypes.POINTER(ICDims), _P, _P, _Z, _P]
+_lib.ic_prefix_attn.restype = _I
+_lib.ic_prefix_attn.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P,
+                                _Z, _P]
+_lib.ic_prefix_attn_workspace_bytes.restype = _Z
+_lib.ic_prefix_attn_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I, _I]
+_lib.ic_attn_mass.restype = _I
+_lib.ic_attn_mass.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P]
+_lib.ic_attn_mass_sparse.restype = _I
+_lib.ic_attn_mass_sparse.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _Z,
+                                     _P]
+_lib.ic_attn_mass_sparse_workspace_bytes.restype = _Z
+_lib.ic_attn_mass_sparse_workspace_bytes.argtypes = [_I, _I, _I]
+_lib.ic_evict_select.restype = _I
+_lib.ic_evict_select.argtypes = [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P]
+_lib.ic_cache_gather.restype = _I
+_lib.ic_cache_gather.argtypes = [_P, _I, _I, _I, _I, _I, ctypes.POINTER(ICCacheCopy), _P]
 
 
 def lib() -> ctypes.CDLL:
@@ -332,6 +355,160 @@ def sparse_attn_no_alloc(q, k, v, idx, q_offset: int = 0, scale: float = 0.0, ou
                                       _ptr(lse, torch.float32, "lse"), _stream(stream))
     _check(rc, "ic_sparse_attn_no_alloc")
     return out, lse
+
+
+def _own_shapes(q, k, name="k"):
+    """(B, Lq, Hq, d, Lk, Hkv) of q [B,Lq,Hq,d] and a cache k [B,Lk,Hkv,d] or
+    [B,Lk,d] (one KV head)."""
+    B, Lq, Hq, d = _dims_of(q, 4, "q")
+    if k.dim() == 4:
+        Lk, Hkv = k.shape[1], k.shape[2]
+        _expect(k, (B, Lk, Hkv, d), name)
+    else:
+        Lk, Hkv = _dims_of(k, 3, name)[1], 1
+        _expect(k, (B, Lk, d), name)
+    return B, Lq, Hq, d, Lk, Hkv
+
+
+def prefix_attn_workspace_bytes(B: int, Lq: int, P: int, S: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(_lib.ic_prefix_attn_workspace_bytes(B, Lq, P, S, Hq, Hkv, d))
+
+
+def prefix_attn(q, k_prefix, v_prefix, k=None, v=None, lens=None, scale: float = 0.0, out=None,
+                lse=None, want_lse: bool = True, ws=None, stream=None):
+    """(out [B,Lq,Hq,d] bf16, lse [B,Lq,Hq] fp32) of a batch that shares the
+    keys k_prefix, v_prefix [P,Hkv,d] (or [P,d]): row i of sequence b also
+    sees its own cache k, v [B,S,Hkv,d] (or [B,S,d]; None: no own cache) up to
+    position lens[b] - Lq + i (lens [B] int32; None: S everywhere).  ws=None
+    allocates the full workspace; pass an empty tensor to run without one."""
+    B, Lq, Hq, d = _dims_of(q, 4, "q")
+    if k_prefix.dim() == 3:
+        P, Hkv = k_prefix.shape[0], k_prefix.shape[1]
+        _expect(k_prefix, (P, Hkv, d), "k_prefix")
+    else:
+        P, Hkv = _dims_of(k_prefix, 2, "k_prefix")[0], 1
+        _expect(k_prefix, (P, d), "k_prefix")
+    _expect(v_prefix, tuple(k_prefix.shape), "v_prefix")
+    S = 0
+    if k is not None or v is not None:
+        if k is None or v is None:
+            raise ValueError("k and v come together")
+        S, own_heads = _own_shapes(q, k)[4:]
+        if own_heads != Hkv:
+            raise ValueError(f"k has {own_heads} heads, k_prefix has {Hkv}")
+        _expect(v, tuple(k.shape), "v")
+    _expect(lens, (B,), "lens")
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty(B, Lq, Hq, device=q.device, dtype=torch.float32)
+    _expect(out, (B, Lq, Hq, d), "out")
+    _expect(lse, (B, Lq, Hq), "lse")
+    if ws is None:
+        nbytes = prefix_attn_workspace_bytes(B, Lq, P, S, Hq, Hkv, d)
+        ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8) if nbytes else None
+    nws = 0 if ws is None else ws.numel() * ws.element_size()
+    rc = _lib.ic_prefix_attn(_ptr(q, torch.bfloat16, "q"),
+                             _ptr(k_prefix, torch.bfloat16, "k_prefix"),
+                             _ptr(v_prefix, torch.bfloat16, "v_prefix"),
+                             _ptr(k, torch.bfloat16, "k"), _ptr(v, torch.bfloat16, "v"),
+                             _ptr(lens, torch.int32, "lens"), B, Lq, P, S, Hq, Hkv, d, float(scale),
+                             _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"),
+                             _ptr(ws, None, "ws") if nws else None, nws, _stream(stream))
+    _check(rc, "ic_prefix_attn")
+    return out, lse
+
+
+def attn_mass(q, k, lse, mass, lens=None, q_offset: int = 0, scale: float = 0.0, stream=None):
+    """Adds to mass [B,Lk] fp32 (returned) the attention weight that every
+    position of k [B,Lk,Hkv,d] (or [B,Lk,d]) received from the rows of q
+    [B,Lq,Hq,d] that see it, summed over rows and heads; lse [B,Lq,Hq] fp32 is
+    what the attention call returned.  Row i sees s <= q_offset + i, or with lens
+    [B] int32 s <= lens[b] - Lq + i (ic_attn_mass)."""
+    B, Lq, Hq, d, Lk, Hkv = _own_shapes(q, k)
+    _expect(lse, (B, Lq, Hq), "lse")
+    _expect(mass, (B, Lk), "mass")
+    _expect(lens, (B,), "lens")
+    rc = _lib.ic_attn_mass(_ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"),
+                           _ptr(lse, torch.float32, "lse"), _ptr(lens, torch.int32, "lens"), B, Lq,
+                           Lk, Hq, Hkv, d, q_offset, float(scale),
+                           _ptr(mass, torch.float32, "mass"), _stream(stream))
+    _check(rc, "ic_attn_mass")
+    return mass
+
+
+def attn_mass_sparse_workspace_bytes(B: int, Lq: int, Lk: int) -> int:
+    return int(_lib.ic_attn_mass_sparse_workspace_bytes(B, Lq, Lk))
+
+
+def attn_mass_sparse(q, k, idx, lse, mass, q_offset: int = 0, scale: float = 0.0, ws=None,
+                     stream=None):
+    """attn_mass over the slots of an index cache idx [B,Lq,k] int32, with
+    the lse sparse_attn returned for them (ic_attn_mass_sparse).  ws=None
+    allocates the workspace (Lq > 1 only)."""
+    B, Lq, Hq, d, Lk, Hkv = _own_shapes(q, k)
+    kslots = _dims_of(idx, 3, "idx")[2]
+    _expect(idx, (B, Lq, kslots), "idx")
+    _expect(lse, (B, Lq, Hq), "lse")
+    _expect(mass, (B, Lk), "mass")
+    if ws is None:
+        nbytes = attn_mass_sparse_workspace_bytes(B, Lq, Lk)
+        ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8) if nbytes else None
+    nws = 0 if ws is None else ws.numel() * ws.element_size()
+    rc = _lib.ic_attn_mass_sparse(_ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"),
+                                  _ptr(idx, torch.int32, "idx"), _ptr(lse, torch.float32, "lse"), B,
+                                  Lq, Lk, Hq, Hkv, d, kslots, q_offset, float(scale),
+                                  _ptr(mass, torch.float32, "mass"),
+                                  _ptr(ws, None, "ws") if nws else None, nws, _stream(stream))
+    _check(rc, "ic_attn_mass_sparse")
+    return mass
+
+
+def evict_select(mass, n_keep: int, lens=None, n_sink: int = 0, n_recent: int = 0, keep=None,
+                 new_lens=None, stream=None):
+    """(keep [B,n_keep] int32, new_lens [B] int32): the ascending positions
+    each cache keeps under a budget of n_keep -- the first n_sink, the last
+    n_recent and the others of most mass [B,Lk] fp32 -- padded with -1
+    (ic_evict_select)."""
+    B, Lk = _dims_of(mass, 2, "mass")
+    _expect(lens, (B,), "lens")
+    if keep is None:
+        keep = torch.empty(B, max(int(n_keep), 0), device=mass.device, dtype=torch.int32)
+    if new_lens is None:
+        new_lens = torch.empty(B, device=mass.device, dtype=torch.int32)
+    _expect(keep, (B, n_keep), "keep")
+    _expect(new_lens, (B,), "new_lens")
+    rc = _lib.ic_evict_select(_ptr(mass, torch.float32, "mass"), _ptr(lens, torch.int32, "lens"), B,
+                              Lk, n_keep, n_sink, n_recent, _ptr(keep, torch.int32, "keep"),
+                              _ptr(new_lens, torch.int32, "new_lens"), _stream(stream))
+    _check(rc, "ic_evict_select")
+    return keep, new_lens
+
+
+def cache_gather(keep, srcs: Sequence[torch.Tensor], dsts: Sequence[torch.Tensor], stream=None):
+    """dst[b, j] = src[b, keep[b, j]] for every pair of tensors src [B,Lk,...]
+    and dst [B,Lk_dst,...] (all with the same Lk and the same Lk_dst) and every
+    slot of keep [B,n_keep] int32 that is not -1; the other rows of dst stay as
+    they were (ic_cache_gather).  Returns dsts."""
+    B, n_keep = _dims_of(keep, 2, "keep")
+    if len(srcs) != len(dsts):
+        raise ValueError(f"{len(srcs)} sources, {len(dsts)} destinations")
+    Lk = srcs[0].shape[1] if srcs and srcs[0].dim() >= 2 else 0
+    Lk_dst = dsts[0].shape[1] if dsts and dsts[0].dim() >= 2 else n_keep
+    copies = (ICCacheCopy * max(len(srcs), 1))()
+    for x, (s, d) in enumerate(zip(srcs, dsts)):
+        _expect(s, (B, Lk) + tuple(s.shape[2:]), f"source {x}")
+        _expect(d, (B, Lk_dst) + tuple(s.shape[2:]), f"destination {x}")
+    for x, (s, d) in enumerate(zip(srcs, dsts)):
+        row = s.element_size()
+        for n in s.shape[2:]:
+            row *= n
+        copies[x] = ICCacheCopy(_ptr(s, None, f"source {x}"), _ptr(d, s.dtype, f"destination {x}"),
+                                row)
+    rc = _lib.ic_cache_gather(_ptr(keep, torch.int32, "keep"), B, Lk, n_keep, Lk_dst, len(srcs),
+                              copies, _stream(stream))
+    _check(rc, "ic_cache_gather")
+    return dsts
 
 
 def make_dims(B, Lq, Lk, q_offset, H_I, d_I, Hq, d, k, scale=0.0, Hkv=1) -> ICDims:
