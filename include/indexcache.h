@@ -377,18 +377,17 @@ int ic_index_overlap(const int32_t *idx_a, const int32_t *idx_b, long long n_row
  * IC_ERR_INVALID_ARG in the device error word.  d in {64, 128}; Hq <= 128 a
  * multiple of Hkv, query head h reads K/V head h / (Hq / Hkv).  scale <= 0
  * selects 1/sqrt(d).
+ * lens is not read when S == 0 and P > 0.  P and S up to 2^30.
  * ws/ws_bytes: device workspace of ic_prefix_attn_workspace_bytes(...) bytes
- * for the partial results of rows whose keys are split over several CTAs;
- * with less (ws may be NULL when ws_bytes is 0) keys are split less or not at
- * all, and results differ only by the rounding of the merges.
+ * for the partial results of rows whose keys are split over several CTAs (may
+ * be NULL when that is 0); less returns IC_ERR_WORKSPACE_TOO_SMALL.
  */
 int ic_prefix_attn(const uint16_t *q, const uint16_t *k_prefix, const uint16_t *v_prefix,
                    const uint16_t *k, const uint16_t *v, const int32_t *lens, int B, int Lq, int P,
                    int S, int Hq, int Hkv, int d, float scale, uint16_t *out, float *lse, void *ws,
                    size_t ws_bytes, ic_stream_t stream);
 
-/* Workspace with which ic_prefix_attn splits keys as it prefers (0 for
- * invalid sizes). */
+/* Workspace ic_prefix_attn needs on the current device (0 for invalid sizes). */
 size_t ic_prefix_attn_workspace_bytes(int B, int Lq, int P, int S, int Hq, int Hkv, int d);
 
 /*

@@ -33,13 +33,103 @@ int evict_cluster(int Lk) {
     return c;
 }
 
+// Sizes whose positions and rows the kernels count in 32 bits.
+int check_prefix_sizes(int B, int Lq, int P, int S, int Hq) {
+    if (P > (1 << 30) || S > (1 << 30))
+        return fail(IC_ERR_UNSUPPORTED, "P=%d, S=%d (supported: up to 2^30)", P, S);
+    if ((long long)B * Lq * Hq > MAX_GRID_X || (long long)B * Lq > MAX_GRID_X / 128)
+        return fail(IC_ERR_UNSUPPORTED, "B=%d, Lq=%d: too many query rows", B, Lq);
+    return IC_OK;
+}
+
+// Work units of a shared-prefix attention and its partials per row.
+struct PrefixGeom {
+    bool shared = false;
+    int p_row_units = 0, p_splits = 0, p_tps = 0, p_streams = 0;
+    int o_row_units = 0, o_splits = 0, o_tps = 0, o_streams = 0;
+    int slots = 0;
+    long long n_prefix = 0, n_own = 0;
+    size_t ws_bytes = 0;
+};
+
+// How finely the keys are split: `s` bounds the steps (one stream's 128 x 128
+// tile, about 0.6 us) of a unit, and the s of the smallest estimated time is
+// taken.  A unit costs its steps and about 3 more to start and end; an own
+// tile counts double (64 KB of K and V for one step); merging a partial row
+// costs the time of writing and reading it.  Units up to the number of SMs run
+// at once, more run in turn, the last half a unit late on average.
+PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int sms) {
+    PrefixGeom g;
+    const int T = ic::PA_TILE, G = Hq / Hkv;
+    const long long rp = (long long)B * Lq * G, ro = (long long)Lq * G;
+    const int p_nt = (P + T - 1) / T, o_nt = std::max(1, (S + T - 1) / T);
+    const bool has_p = P > 0, has_o = S > 0 || P == 0;        // no key at all: the own units write zeros
+    g.shared = rp > T;
+    const int per_step = g.shared ? 2 : 1;
+    if (has_p) g.p_row_units = (int)((rp + T * per_step - 1) / (T * per_step));
+    if (has_o) g.o_row_units = (int)((ro + T - 1) / T);
+    const long long n_pu = (long long)g.p_row_units * Hkv, n_ou = (long long)B * g.o_row_units * Hkv;
+    const double p_work = (double)n_pu * p_nt * per_step, o_work = 2.0 * n_ou * o_nt;
+    const double merge = (double)B * Lq * Hq * d * 1.65e-6;
+    const int s_max = std::max(has_p ? p_nt * per_step : 1, has_o ? o_nt : 1);
+    double best = -1.0;
+    for (int s = 1;; s = std::min(s_max, s + std::max(1, s / 8))) {
+        const int p_tps = std::min(std::max(1, s / per_step), std::max(1, p_nt));
+        const int o_tps = std::min(std::max(1, s / 2), o_nt);
+        const int p_sp = has_p ? (p_nt + p_tps - 1) / p_tps : 0, o_sp = has_o ? (o_nt + o_tps - 1) / o_tps : 0;
+        const int p_str = g.shared ? 1 : std::min(2, p_tps), o_str = std::min(2, o_tps);
+        const long long slots = (long long)p_sp * p_str + (long long)o_sp * o_str;
+        const double n = (double)n_pu * p_sp + (double)n_ou * o_sp;
+        const double unit = 3.0 + std::max(has_p ? p_tps * per_step : 0, has_o ? 2 * o_tps : 0);
+        double est = n <= sms ? unit : std::max(unit, (p_work + o_work + 3.0 * n) / sms + 0.5 * unit);
+        if (slots > 1) est += merge * slots;
+        if (n < 2147483647.0 && (best < 0.0 || est < best)) {
+            best = est;
+            g.p_tps = p_tps; g.o_tps = o_tps;
+            g.p_splits = p_sp; g.o_splits = o_sp;
+            g.p_streams = has_p ? p_str : 0; g.o_streams = has_o ? o_str : 0;
+            g.slots = (int)slots;
+        }
+        if (s >= s_max) break;
+    }
+    g.n_prefix = n_pu * g.p_splits;
+    g.n_own = n_ou * g.o_splits;
+    if (g.slots > 1) g.ws_bytes = (size_t)B * Lq * Hq * g.slots * (d + 1) * sizeof(float);
+    return g;
+}
+
+// A bf16 tensor map of `rank` dimensions, 128-byte swizzled boxes of 64
+// columns; what lies outside reads as zeros.
+int make_tmap(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+              const uint32_t* box) {
+    int rc = get_encode();
+    if (rc) return rc;
+    cuuint64_t gd[5], gs[4];
+    cuuint32_t bx[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        gd[i] = dims[i];
+        bx[i] = box[i];
+        es[i] = 1;
+        if (i + 1 < rank) gs[i] = strides[i];
+    }
+    CUresult r = encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), gd,
+                          gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(IC_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return IC_OK;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t ic_prefix_attn_workspace_bytes(int B, int Lq, int P, int S, int Hq, int Hkv, int d) {
-    (void)B; (void)Lq; (void)P; (void)S; (void)Hq; (void)Hkv; (void)d;
-    return 0;
+    if (B <= 0 || Lq <= 0 || P < 0 || S < 0 || check_cache_heads(Hq, Hkv, d) ||
+        check_prefix_sizes(B, Lq, P, S, Hq))
+        return 0;
+    int dev, sms;
+    if (device_setup(&dev, &sms)) sms = 148;
+    return prefix_geom(B, Lq, P, S, Hq, Hkv, d, sms).ws_bytes;
 }
 
 int ic_prefix_attn(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* v_prefix,
@@ -61,25 +151,62 @@ int ic_prefix_attn(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* 
         return fail(IC_ERR_UNSUPPORTED, "lse and lens must be 4-byte aligned");
     if (ws_bytes > 0 && !ws) return fail(IC_ERR_INVALID_ARG, "ws is NULL but ws_bytes > 0");
     if (ws && !aligned16(ws)) return fail(IC_ERR_UNSUPPORTED, "ws must be 16-byte aligned");
-    const long long rows = (long long)B * Lq * Hq;
-    if (rows > MAX_GRID_X) return fail(IC_ERR_UNSUPPORTED, "B*Lq*Hq = %lld too large", rows);
+    if ((rc = check_prefix_sizes(B, Lq, P, S, Hq))) return rc;
     int dev, sms;
     if ((rc = device_setup(&dev, &sms))) return rc;
+    const PrefixGeom g = prefix_geom(B, Lq, P, S, Hq, Hkv, d, sms);
+    if (ws_bytes < g.ws_bytes)
+        return fail(IC_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", ws_bytes, g.ws_bytes);
+    CUtensorMap tkp{}, tvp{}, tk{}, tv{};
+    const uint64_t hd = (uint64_t)Hkv * d;
+    if (P > 0) {
+        const uint64_t dims[3] = {(uint64_t)d, (uint64_t)Hkv, (uint64_t)P};
+        const uint64_t strides[2] = {(uint64_t)d * 2, hd * 2};
+        const uint32_t box[3] = {64, 1, ic::PA_TILE};
+        if ((rc = make_tmap(&tkp, k_prefix, 3, dims, strides, box))) return rc;
+        if ((rc = make_tmap(&tvp, v_prefix, 3, dims, strides, box))) return rc;
+    }
+    if (S > 0) {
+        const uint64_t dims[4] = {(uint64_t)d, (uint64_t)Hkv, (uint64_t)S, (uint64_t)B};
+        const uint64_t strides[3] = {(uint64_t)d * 2, hd * 2, hd * 2 * S};
+        const uint32_t box[4] = {64, 1, ic::PA_TILE, 1};
+        if ((rc = make_tmap(&tk, k, 4, dims, strides, box))) return rc;
+        if ((rc = make_tmap(&tv, v, 4, dims, strides, box))) return rc;
+    }
+    const long long rows = (long long)B * Lq * Hq;
     ic::PrefixAttnArgs a{};
     a.q = reinterpret_cast<const __nv_bfloat16*>(q);
-    a.kp = reinterpret_cast<const __nv_bfloat16*>(k_prefix);
-    a.vp = reinterpret_cast<const __nv_bfloat16*>(v_prefix);
-    a.k = reinterpret_cast<const __nv_bfloat16*>(k);
-    a.v = reinterpret_cast<const __nv_bfloat16*>(v);
     a.lens = lens;
     a.out = reinterpret_cast<__nv_bfloat16*>(out);
     a.lse = lse;
-    a.B = B; a.Lq = Lq; a.P = P; a.S = S; a.Hq = Hq; a.Hkv = Hkv;
+    a.part_o = reinterpret_cast<float*>(ws);
+    a.part_lse = a.part_o ? a.part_o + rows * g.slots * d : nullptr;
+    a.B = B; a.Lq = Lq; a.P = P; a.S = S; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
+    a.slots = g.slots;
+    a.n_prefix = (int)g.n_prefix;
+    a.shared = g.shared ? 1 : 0;
+    a.p_row_units = g.p_row_units; a.p_splits = g.p_splits; a.p_tps = g.p_tps; a.p_streams = g.p_streams;
+    a.o_row_units = g.o_row_units; a.o_splits = g.o_splits; a.o_tps = g.o_tps; a.o_streams = g.o_streams;
+    a.o_slot0 = g.p_splits * g.p_streams;
     a.scale_log2 = scale_log2_of(scale, d);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (d == 64) ic::prefix_attn_kernel<64><<<(unsigned)rows, 128, 0, st>>>(a);
-    else ic::prefix_attn_kernel<128><<<(unsigned)rows, 128, 0, st>>>(a);
-    return launched(cudaGetLastError(), "prefix_attn launch");
+    const unsigned grid = (unsigned)(g.n_prefix + g.n_own);
+    if (d == 64)
+        ic::prefix_attn_kernel<64><<<grid, ic::PA_THREADS, ic::PrefixSmem<64>::ALLOC, st>>>(tkp, tvp, tk, tv, a);
+    else
+        ic::prefix_attn_kernel<128><<<grid, ic::PA_THREADS, ic::PrefixSmem<128>::ALLOC, st>>>(tkp, tvp, tk, tv, a);
+    if (launched(cudaGetLastError(), "prefix_attn launch")) return IC_ERR_CUDA;
+    if (g.slots == 1) return IC_OK;
+    const bool wide = g.slots > 8;
+    const unsigned cg = (unsigned)(wide ? rows : (rows + 3) / 4);
+    if (d == 64) {
+        if (wide) ic::prefix_combine_kernel<64, true><<<cg, 128, 0, st>>>(a, rows);
+        else ic::prefix_combine_kernel<64, false><<<cg, 128, 0, st>>>(a, rows);
+    } else {
+        if (wide) ic::prefix_combine_kernel<128, true><<<cg, 128, 0, st>>>(a, rows);
+        else ic::prefix_combine_kernel<128, false><<<cg, 128, 0, st>>>(a, rows);
+    }
+    return launched(cudaGetLastError(), "prefix_attn combine launch");
 }
 
 int ic_attn_mass(const uint16_t* q, const uint16_t* k, const float* lse, const int32_t* lens, int B,

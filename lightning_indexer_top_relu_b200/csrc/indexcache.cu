@@ -804,6 +804,10 @@ int device_setup(int* dev_out, int* sms_out) {
                              cudaFuncAttributeMaxDynamicSharedMemorySize, ic::SaSmem<64>::BYTES);
         cudaFuncSetAttribute(ic::sparse_attn_kernel<128>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, ic::SaSmem<128>::BYTES);
+        cudaFuncSetAttribute(ic::prefix_attn_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ic::PrefixSmem<64>::ALLOC);
+        cudaFuncSetAttribute(ic::prefix_attn_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ic::PrefixSmem<128>::ALLOC);
         cudaFuncSetAttribute(ic::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ic::EvictSmem::bytes(ic::EV_CACHE_MAX));
         e = cudaGetLastError();

@@ -4,23 +4,68 @@
 // over the first n_vis(b, i) = clamp(lens[b] - Lq + i + 1, 0, S) keys of its
 // own cache:
 //   z = scale * q . K,  out = sum softmax(z) V,  lse = ln sum e^z.
-// Query head h reads K/V head h / (Hq / Hkv).
+// Query head h reads K/V head j = h / G, G = Hq / Hkv.
+//
+// The softmax splits over the keys: a partial result (O / l, log2-sum-exp) of
+// any key range merges exactly with those of the others.  So the prefix is
+// one attention of all B * Lq * G rows of a K/V head over the same P keys --
+// each K/V tile is read once for 256 rows instead of once per sequence --
+// and each sequence's own cache a small one of its Lq * G rows.  Every work
+// unit of either kind is one CTA; partials go to the workspace and
+// prefix_combine_kernel merges them.
+//
+// One CTA (1 per SM): two streams, each a 128-row query tile (TMEM lanes)
+// with its own score buffer, output accumulator and softmax warpgroup, so one
+// stream's exponentials overlap the other's MMAs.
+//   shared units (more than 128 rows over the prefix): the streams are two row
+//     tiles, both of which use every K/V tile;
+//   split units (own caches, or a prefix with at most 128 rows): both streams
+//     hold the same rows and take alternate K/V tiles (two partials).
+// Step n of a unit belongs to stream n & 1 and key tile n >> 1 (shared) or n
+// (split).
+//   warp 0      TMA: 128-key tiles of K and V, alternately, into one ring.
+//   warp 1      TMEM allocation and MMA issue.  S(n) = Q K^T (M=128, N=128),
+//               then O += P(n-1) V.  P comes from TMEM, V from its [keys, d]
+//               tile as an MN-major operand (no transposed copy).  S(n)
+//               overwrites the columns of P(n-2), so it is issued when P(n-2) V
+//               has completed.
+//   warps 4-7, 8-11  the softmax of stream 0 / 1: thread = row = TMEM lane.
+//               Scores come in chunks of 32 columns; the probabilities against
+//               the running maximum are packed to bf16 and stored over the
+//               score columns.  Their rounding (2^-8 of each) is what the bf16
+//               matrix instruction takes; the row sum is taken before it, in
+//               fp32.  The maximum is raised lazily: bf16 and fp32 keep their
+//               relative precision at any scale, so the exponent base only moves
+//               when a tile's sum passes 2^32 (and on the first keys seen).
 #pragma once
 
 #include "common.cuh"
+#include "dense_attn.cuh"
 
 namespace ic {
 
+constexpr int PA_THREADS = 384;                   // a control warpgroup and one per stream
+// Registers a thread: launched with 168 (65536 / 384, rounded down to 8); the
+// control warpgroup gives some up for the softmax ones.
+constexpr int PA_REGS_CONTROL = 80, PA_REGS_SOFTMAX = 208;
+static_assert(PA_REGS_CONTROL + 2 * PA_REGS_SOFTMAX <= 3 * 168, "register split of the launch");
+constexpr int PA_TILE = 128;                      // keys per tile and rows per stream
+constexpr float PA_SUM_MAX = 4294967296.0f;       // 2^32
+
 struct PrefixAttnArgs {
     const __nv_bfloat16* q;     // [B, Lq, Hq, D]
-    const __nv_bfloat16* kp;    // [P, Hkv, D]
-    const __nv_bfloat16* vp;
-    const __nv_bfloat16* k;     // [B, S, Hkv, D]
-    const __nv_bfloat16* v;
     const int32_t* lens;        // [B] or null (S)
     __nv_bfloat16* out;         // [B, Lq, Hq, D]
     float* lse;                 // [B, Lq, Hq] or null
-    int B, Lq, P, S, Hq, Hkv;
+    float* part_o;              // [B * Lq * Hq, slots, D]
+    float* part_lse;            // [B * Lq * Hq, slots] log2-sum-exp
+    int B, Lq, P, S, Hq, Hkv, G;
+    int slots;                  // partials per row; 1: out and lse are written directly
+    // prefix units: row tiles (pairs of them when shared) x key splits x Hkv
+    // (tps: tiles per split; streams: partials of a unit)
+    int n_prefix, shared, p_row_units, p_splits, p_tps, p_streams;
+    // own units: B x row tiles x key splits x Hkv; their partials start at slot o_slot0
+    int o_row_units, o_splits, o_tps, o_slot0, o_streams;
     float scale_log2;
 };
 
@@ -36,59 +81,491 @@ __device__ __forceinline__ int seq_len(const int32_t* lens, int b, int cap) {
     return n;
 }
 
-// One CTA per (b, i, h): its four warps take every fourth key each, with an
-// online softmax in fp32, and merge at the end.
 template <int D>
-__global__ void __launch_bounds__(128)
-prefix_attn_kernel(const PrefixAttnArgs a) {
-    constexpr int E = D / 32;
-    __shared__ float so[4][D], sm[4], sl[4];
+struct PrefixSmem {
+    static constexpr int STAGE = PA_TILE * D * 2;            // one K or V tile (D / 64 boxes)
+    static constexpr int STAGES = D == 128 ? 5 : 10;
+    static constexpr int OFF_Q = 0;                          // two row tiles
+    static constexpr int OFF_KV = OFF_Q + 2 * STAGE;
+    static constexpr int OFF_BAR = OFF_KV + STAGES * STAGE;
+    static constexpr int N_BARS = 2 * STAGES + 8;
+    static constexpr int OFF_SLOT = OFF_BAR + N_BARS * 8;
+    static constexpr int BYTES = OFF_SLOT + 16;
+    static constexpr int ALLOC = BYTES + 1024;               // slack for the 1024-byte alignment
+    static_assert(ALLOC <= MAX_DYN_SMEM, "shared memory of one CTA");
+};
+
+// Waits for the loads of tcgen05.ld into r: the registers pass through, so no
+// use of them moves ahead of the wait.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                   "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                   "+r"(r[31])::"memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Shared-memory matrix descriptors as {low, high} words, so that stepping
+// through a tile is one 32-bit add of bytes / 16 to the low word.  High word:
+// stride byte offset 1024 (the next 8 rows of 128 B), version 1, 128-byte
+// swizzle.  Low word: address / 16 and the leading byte offset -- for a K-major
+// operand unused (1), for an MN-major one (64 MN elements x 8 K rows per
+// 1024-byte atom) the distance of the next 64 MN elements, one TMA box on.
+constexpr uint32_t SW128_DESC_HI = (uint32_t)(1024 >> 4) | 1u << 14 | 2u << 29;
+
+__device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t smem_addr, uint32_t leading_bytes) {
+    return ((smem_addr & 0x3FFFFu) >> 4) | (leading_bytes >> 4) << 16;
+}
+
+// D[tmem] (+)= A * B^T, kind::f16, operands by descriptor low words (A from
+// shared memory or, K-major by nature, from TMEM).
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(SW128_DESC_HI), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(SW128_DESC_HI), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+constexpr uint32_t IDESC_B_MN_MAJOR = 1u << 16;
+
+// tmap_kp, tmap_vp: {D, Hkv, P}, box {64, 1, 128}; tmap_k, tmap_v: {D, Hkv, S,
+// B}, box {64, 1, 128, 1}; keys past the end read as zeros.
+template <int D>
+__global__ void __launch_bounds__(PA_THREADS, 1)
+prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_constant__ CUtensorMap tmap_vp,
+                   const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                   const PrefixAttnArgs a) {
+    using S = PrefixSmem<D>;
+    constexpr int NST = S::STAGES;
+    constexpr int BOX = PA_TILE * 128;                       // bytes of one 64-column box
+    constexpr uint32_t O_COL = 256;
+    extern __shared__ uint8_t pa_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row = blockIdx.x;
-    const int h = (int)(row % a.Hq);
-    const long long bi = row / a.Hq;
-    const int i = (int)(bi % a.Lq), b = (int)(bi / a.Lq);
-    const int j = h / (a.Hq / a.Hkv);
-    const int n = seq_len(a.lens, b, a.S);
-    const int vis = (int)min((long long)a.S, max(0LL, (long long)n - a.Lq + i + 1));
-    float q[E], o[E] = {};
-    for (int e = 0; e < E; ++e) q[e] = __bfloat162float(a.q[row * D + e * 32 + lane]) * a.scale_log2;
-    float m = -INFINITY, l = 0.0f;
-    for (int part = 0; part < 2; ++part) {
-        const long long nk = part ? vis : a.P;
-        const __nv_bfloat16* kk = part ? a.k + (long long)b * a.S * a.Hkv * D : a.kp;
-        const __nv_bfloat16* vv = part ? a.v + (long long)b * a.S * a.Hkv * D : a.vp;
-        for (long long s = warp; s < nk; s += 4) {
-            const long long off = (s * a.Hkv + j) * D;
-            float z = 0.0f;
-            for (int e = 0; e < E; ++e) z = fmaf(q[e], __bfloat162float(kk[off + e * 32 + lane]), z);
-            for (int w = 16; w >= 1; w >>= 1) z += __shfl_xor_sync(0xffffffffu, z, w);
-            const float mn = fmaxf(m, z);
-            if (mn == -INFINITY) continue;
-            const float al = exp2f(m - mn), p = exp2f(z - mn);
-            for (int e = 0; e < E; ++e)
-                o[e] = o[e] * al + p * __bfloat162float(vv[off + e * 32 + lane]);
-            l = l * al + p;
-            m = mn;
+
+    // ---------------- the unit: rows r0 .. of one K/V head, keys [key0, key_end)
+    int u = blockIdx.x;
+    const bool prefix = u < a.n_prefix;
+    int j, r0, bi0, n_rows, key0, key_end, slot, b = 0, own_len = 0;
+    if (prefix) {
+        const int ru = u % a.p_row_units;
+        u /= a.p_row_units;
+        const int sp = u % a.p_splits;
+        j = u / a.p_splits;
+        bi0 = 0;
+        n_rows = a.B * a.Lq * a.G;
+        r0 = ru * (a.shared ? 2 * PA_TILE : PA_TILE);
+        key0 = sp * a.p_tps * PA_TILE;
+        key_end = (int)min((long long)a.P, (long long)key0 + (long long)a.p_tps * PA_TILE);
+        slot = a.p_streams * sp;
+    } else {
+        u -= a.n_prefix;
+        const int sp = u % a.o_splits;
+        u /= a.o_splits;
+        const int ru = u % a.o_row_units;
+        u /= a.o_row_units;
+        j = u % a.Hkv;
+        b = u / a.Hkv;
+        bi0 = b * a.Lq;
+        n_rows = a.Lq * a.G;
+        r0 = ru * PA_TILE;
+        own_len = seq_len(a.lens, b, a.S);
+        const int i_last = (min(r0 + PA_TILE, n_rows) - 1) / a.G;
+        const int vis = max(0, own_len - a.Lq + i_last + 1);           // of the last row: the most
+        key0 = sp * a.o_tps * PA_TILE;
+        key_end = (int)min((long long)vis, (long long)key0 + (long long)a.o_tps * PA_TILE);
+        slot = a.o_slot0 + a.o_streams * sp;
+    }
+    const bool shared = prefix && a.shared;
+    const int nt = key_end > key0 ? (key_end - key0 + PA_TILE - 1) / PA_TILE : 0;
+    const int steps = shared ? 2 * nt : nt;
+
+    // ---------------- softmax threads: their row
+    const int stream = warp >= 8 ? 1 : 0;
+    const int wq = warp & 3;                                           // TMEM lane quarter
+    const int tr = wq * 32 + lane;                                     // row of the tile
+    const int r = r0 + (shared ? stream * PA_TILE : 0) + tr;
+    const bool row_ok = warp >= 4 && r < n_rows;
+    const int bi = bi0 + r / a.G;                                      // b * Lq + i
+    const long long row = (long long)bi * a.Hq + j * a.G + r % a.G;
+    const int vis = !row_ok ? 0 : (prefix ? a.P : max(0, own_len - a.Lq + r / a.G + 1));
+    const int my_slot = slot + (shared ? 0 : stream);
+    const int my_steps = (steps + 1 - stream) >> 1;
+    // a split unit writes one partial per stream that could have a tile
+    const bool writes = row_ok && (shared || stream < (prefix ? a.p_streams : a.o_streams));
+
+    if (nt == 0) {                                                     // nothing visible here
+        if (writes) {
+            if (a.slots > 1) {
+                a.part_lse[row * a.slots + my_slot] = -INFINITY;
+            } else {
+                for (int c = 0; c < D / 8; ++c)
+                    reinterpret_cast<uint4*>(a.out + row * D)[c] = make_uint4(0, 0, 0, 0);
+                if (a.lse) a.lse[row] = -INFINITY;
+            }
+        }
+        return;
+    }
+    uint8_t* smem = align_smem_1024(pa_raw, S::BYTES);
+    if (smem == nullptr) return;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
+    uint64_t* full = bars;                       // [NST]
+    uint64_t* empty = bars + NST;                // [NST]
+    uint64_t* q_full = bars + 2 * NST;
+    uint64_t* s_full = bars + 2 * NST + 1;       // [2]
+    uint64_t* p_full = bars + 2 * NST + 3;       // [2]
+    uint64_t* o_full = bars + 2 * NST + 5;       // [2]
+    uint64_t* mma_done = bars + 2 * NST + 7;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_SLOT);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(q_full, 256);
+        mbar_init(mma_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+            mbar_init(&o_full[i], 1);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PA_REGS_CONTROL));
+        if (warp == 0 && lane == 0) {
+            const CUtensorMap* mk = prefix ? &tmap_kp : &tmap_k;
+            const CUtensorMap* mv = prefix ? &tmap_vp : &tmap_v;
+            tma_prefetch_desc(mk);
+            tma_prefetch_desc(mv);
+            const int items = 2 * nt;                                  // K(0) V(0) K(1) V(1) ...
+            int it = 0;
+            for (; it < items; ++it) {
+                const int st = it % NST;
+                if (it >= NST && !mbar_wait(&empty[st], ((it / NST) & 1) ^ 1)) break;
+                uint8_t* dst = smem + S::OFF_KV + st * S::STAGE;
+                const CUtensorMap* m = (it & 1) ? mv : mk;
+                const int key = key0 + (it >> 1) * PA_TILE;
+                mbar_arrive_expect_tx(&full[st], (uint32_t)S::STAGE);
+                for (int kb = 0; kb < D / 64; ++kb) {
+                    if (prefix) tma_load_3d(dst + kb * BOX, m, &full[st], kb * 64, j, key);
+                    else tma_load_4d(dst + kb * BOX, m, &full[st], kb * 64, j, key, b);
+                }
+            }
+            // never leave with copies in flight
+            for (int c = max(0, it - NST); c < it; ++c) mbar_wait(&full[c % NST], (c / NST) & 1);
+        }
+        if (warp == 1 && lane == 0) {
+            constexpr uint32_t idesc_s = idesc_bf16_f32(128, PA_TILE);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(128, D) | IDESC_B_MN_MAJOR;
+            const uint32_t q_lo = sw128_desc_lo(smem_u32(smem + S::OFF_Q), 16);
+            const uint32_t kv_addr = smem_u32(smem + S::OFF_KV);
+            bool ok = mbar_wait(q_full, 0);
+            for (int n = 0; n <= steps && ok; ++n) {
+                if (n < steps) {
+                    const int s = n & 1, t = shared ? n >> 1 : n, item = 2 * t, st = item % NST;
+                    if (!(ok = mbar_wait(&full[st], (item / NST) & 1))) break;
+                    if (n >= 2 && !(ok = mbar_wait(&o_full[s], ((n >> 1) - 1) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t qa = q_lo + (uint32_t)(shared ? s * (S::STAGE >> 4) : 0);
+                    const uint32_t ka = sw128_desc_lo(kv_addr + st * S::STAGE, 16);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t o = (uint32_t)((kk >> 2) * BOX + (kk & 3) * 32) >> 4;
+                        tc_mma_ss(tmem + (uint32_t)(s * PA_TILE), qa + o, ka + o, idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(&s_full[s]);
+                    if (!shared || s == 1) tc_commit(&empty[st]);
+                }
+                if (n > 0) {
+                    const int m = n - 1, s = m & 1, t = shared ? m >> 1 : m, item = 2 * t + 1, st = item % NST;
+                    if (!(ok = mbar_wait(&full[st], (item / NST) & 1))) break;
+                    if (!(ok = mbar_wait(&p_full[s], (m >> 1) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t va = sw128_desc_lo(kv_addr + st * S::STAGE, BOX);
+#pragma unroll
+                    for (int kk = 0; kk < PA_TILE / 16; ++kk)
+                        tc_mma_ts(tmem + O_COL + (uint32_t)(s * D), tmem + (uint32_t)(s * PA_TILE + kk * 8),
+                                  va + (uint32_t)(kk * 2048 >> 4), idesc_o, (m >= 2 || kk > 0) ? 1u : 0u);
+                    tc_commit(&o_full[s]);
+                    if (!shared || s == 1) tc_commit(&empty[st]);
+                }
+            }
+            // the MMAs this thread issued are done before TMEM is freed
+            tc_commit(mma_done);
+            mbar_wait(mma_done, 0);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PA_REGS_SOFTMAX));
+        // the row's query to shared memory (rows past the last are zero);
+        // split units have one tile, which the first warpgroup writes
+        if (shared || stream == 0) {
+            const uint4* src = reinterpret_cast<const uint4*>(a.q + row * D);
+            uint8_t* dst = smem + S::OFF_Q + (shared ? stream * S::STAGE : 0) + tr * 128;
+            uint4 v[D / 8];
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) v[c] = row_ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4*>(dst + (c >> 3) * BOX + (((c & 7) ^ (tr & 7)) << 4)) = v[c];
+            fence_proxy_async_smem();
+        }
+        mbar_arrive(q_full);
+
+        const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+        const uint32_t sb = tmem + lane_base + (uint32_t)(stream * PA_TILE);
+        const uint32_t ob = tmem + lane_base + O_COL + (uint32_t)(stream * D);
+        const float sc = a.scale_log2;
+        float m_used = -INFINITY, l_run = 0.0f;
+        bool ok = true;
+        for (int i = 0; i < my_steps; ++i) {
+            const int t = shared ? i : 2 * i + stream;
+            const int key = key0 + t * PA_TILE;
+            const int nv = min(vis, key_end) - key;                    // columns of the tile this row sees
+            const bool masked = __any_sync(0xffffffffu, nv < PA_TILE);
+            // waits are warp-uniform: the TMEM accesses below are warp-collective
+            if (!__all_sync(0xffffffffu, mbar_wait(&s_full[stream], i & 1))) { ok = false; break; }
+            tc_fence_after();
+            uint32_t pk[PA_TILE / 2];
+            float rs = 0.0f;
+            // probabilities of the tile (bf16 pairs) against `base`, and their sum
+            auto softmax_tile = [&](float base) {
+                float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
+                uint32_t v[2][32];
+                tmem_ld_32x32b_x32(sb, v[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld_wait(v[c & 1]);
+                    if (c < 3) tmem_ld_32x32b_x32(sb + (c + 1) * 32, v[(c + 1) & 1]);
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c * 32 + e >= nv) v[c & 1][e] = 0xff800000u;      // -inf
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[c & 1][e]),
+                                                                __uint_as_float(v[c & 1][e + 1])), sc2, nb2);
+                        const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                        acc[(e >> 1) & 1] = __fadd2_rn(acc[(e >> 1) & 1], p);
+                        __nv_bfloat162 pp = __floats2bfloat162_rn(p.x, p.y);
+                        pk[c * 16 + (e >> 1)] = *reinterpret_cast<uint32_t*>(&pp);
+                    }
+                }
+                const float2 s2 = __fadd2_rn(acc[0], acc[1]);
+                rs = s2.x + s2.y;
+            };
+            // Every branch around TMEM accesses is warp-uniform.  Rows that see
+            // nothing of the tile need no maximum (their probabilities are 0).
+            const bool fresh = m_used == -INFINITY;
+            if (!__any_sync(0xffffffffu, nv > 0)) {
+#pragma unroll
+                for (int e = 0; e < PA_TILE / 2; ++e) pk[e] = 0u;
+            } else if (!__all_sync(0xffffffffu, fresh && nv > 0)) {
+                softmax_tile(fresh ? 0.0f : m_used);
+            }
+            const bool need_max = nv > 0 && (fresh || !(rs <= PA_SUM_MAX));
+            if (__any_sync(0xffffffffu, need_max)) {
+                // the tile's maximum; rows that need it move their base to it
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(sb + c * 32, v);
+                    tmem_ld_wait(v);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c * 32 + e < nv) mx = fmaxf(mx, __uint_as_float(v[e]));
+                }
+                const float m_new = need_max ? fmaxf(m_used, mx * sc) : m_used;
+                const float alpha = m_new == m_used ? 1.0f : ex2_approx(m_used - m_new);   // 0 on a first raise
+                if (i > 0) {
+                    // S(i) was issued after P(i-1) V(i-1) completed: O is at rest
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(ob + c * 32, o);
+                        tmem_ld_wait(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st_32x32b_x32(ob + c * 32, o);
+                    }
+                }
+                l_run *= alpha;
+                m_used = m_new;
+                softmax_tile(m_new == -INFINITY ? 0.0f : m_new);
+            }
+            l_run += rs;
+            tmem_st_32x32b_x32(sb, *reinterpret_cast<uint32_t (*)[32]>(&pk[0]));
+            tmem_st_32x32b_x32(sb + 32, *reinterpret_cast<uint32_t (*)[32]>(&pk[32]));
+            tmem_st_wait();
+            if (!prefix && key + PA_TILE > own_len) {
+                // rows of V past the sequence's length may hold anything: zero
+                // them, since 0 * NaN would reach every output
+                const int item = 2 * t + 1, st = item % NST;
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (item / NST) & 1))) { ok = false; break; }
+                if (key + tr >= own_len) {
+                    uint8_t* vrow = smem + S::OFF_KV + st * S::STAGE + tr * 128;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        *reinterpret_cast<uint4*>(vrow + (c >> 3) * BOX + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            tc_fence_before();
+            mbar_arrive(&p_full[stream]);
+        }
+        if (ok && my_steps > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[stream], (my_steps - 1) & 1));
+            tc_fence_after();
+        }
+        if (ok) {                                   // uniform across the warp
+            const float lse2 = l_run == 0.0f ? -INFINITY : m_used + log2f(l_run);
+            const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+            if (writes) {
+                if (a.slots > 1) a.part_lse[row * a.slots + my_slot] = lse2;
+                else if (a.lse) a.lse[row] = lse2 * LN2;
+            }
+            if (my_steps > 0) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tmem_ld_32x32b_x32(ob + c * 32, o);
+                    tmem_ld_wait(o);
+                    if (!writes) continue;
+                    // a row that saw nothing has P = 0: its O is 0 or, from
+                    // non-finite V, NaN; it is written as 0
+                    float f[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] = l_run == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
+                    if (a.slots > 1) {
+                        float4* dst = reinterpret_cast<float4*>(a.part_o + (row * a.slots + my_slot) * D + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                __nv_bfloat162 pp = __floats2bfloat162_rn(f[8 * e + 2 * x], f[8 * e + 2 * x + 1]);
+                                w[x] = *reinterpret_cast<uint32_t*>(&pp);
+                            }
+                            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+            }
         }
     }
-    for (int e = 0; e < E; ++e) so[warp][e * 32 + lane] = o[e];
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
+    tc_fence_before();
     __syncthreads();
-    const float M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float f[4], L = 0.0f;
-    for (int w = 0; w < 4; ++w) {
-        f[w] = M == -INFINITY ? 0.0f : exp2f(sm[w] - M);
-        L += f[w] * sl[w];
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
-    for (int c = threadIdx.x; c < D; c += 128) {
-        const float acc = f[0] * so[0][c] + f[1] * so[1][c] + f[2] * so[2][c] + f[3] * so[3][c];
-        a.out[row * D + c] = __float2bfloat16_rn(L > 0.0f ? acc / L : 0.0f);
+}
+
+// Merges the partials of each row: out = sum_s w_s O_s / sum_s w_s with
+// w_s = 2^(lse2_s - max).  A CTA of four warps takes one row, each warp every
+// fourth partial (WIDE: many partials), or four rows, a warp each.
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(128)
+prefix_combine_kernel(const PrefixAttnArgs a, long long n_rows) {
+    constexpr int E = D / 32;                                   // output columns a lane
+    __shared__ float so[4][D], sw[4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = WIDE ? (long long)blockIdx.x : (long long)blockIdx.x * 4 + warp;
+    if (row >= n_rows) return;                                  // WIDE: every row exists
+    const float* pl = a.part_lse + row * a.slots;
+    const float* po = a.part_o + row * a.slots * D + lane * E;
+    float M = -INFINITY;
+    for (int s = lane; s < a.slots; s += 32) M = fmaxf(M, pl[s]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float W = 0.0f, acc[E] = {};
+    constexpr int STEP = WIDE ? 4 : 1, UN = 4;
+    for (int s0 = WIDE ? warp : 0; s0 < a.slots; s0 += STEP * UN) {
+        float v[UN][E], w[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int s = s0 + u * STEP;
+            const float l = s < a.slots ? pl[s] : -INFINITY;
+            w[u] = l == -INFINITY ? 0.0f : exp2f(l - M);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[u][e] = 0.0f;
+            if (l != -INFINITY) {                               // an empty partial's O is not written
+                if (E == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(po + (long long)s * D);
+                else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(po + (long long)s * D);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            W += w[u];
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(w[u], v[u][e], acc[e]);
+        }
     }
-    if (a.lse && threadIdx.x == 0) a.lse[row] = L > 0.0f ? (M + log2f(L)) * LN2 : -INFINITY;
+    if (WIDE) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
+        if (lane == 0) sw[warp] = W;
+        __syncthreads();
+        if (warp > 0) return;
+        W = sw[0] + sw[1] + sw[2] + sw[3];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = so[0][lane * E + e] + so[1][lane * E + e] + so[2][lane * E + e] + so[3][lane * E + e];
+    }
+    const float inv = W == 0.0f ? 0.0f : 1.0f / W;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+        __nv_bfloat162 pp = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        w[e] = *reinterpret_cast<uint32_t*>(&pp);
+    }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + lane * E);
+    if (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[E / 2 - 1]);
+    else dst[0] = w[0];
+    if (a.lse && lane == 0) a.lse[row] = W == 0.0f ? -INFINITY : (M + log2f(W)) * LN2;
 }
 
 }  // namespace ic

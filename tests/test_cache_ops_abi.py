@@ -44,7 +44,9 @@ def test_prefix_attn_refusals(ic):
     assert call(Hq=8, Hkv=16) == 2
     assert call(lse=0x8002) == 2 and call(lens=0x6002) == 2
     assert call(wsb=64) == 1 and call(ws=0x9008, wsb=64) == 2
+    assert call(P=(1 << 30) + 1) == 2 and call(S=(1 << 30) + 1) == 2 and call(B=1 << 24, Lq=16) == 2
     assert call(B=0) == 0 and call(Lq=0) == 0
+    assert ic.prefix_attn_workspace_bytes(3, 2, 4096, 256, 16, 2, 64) >= 2 * 3 * 2 * 16 * 65 * 4
     assert ic.prefix_attn_workspace_bytes(0, 1, 64, 32, 16, 1, 128) == 0
     assert ic.prefix_attn_workspace_bytes(1, 1, 64, 32, 16, 3, 128) == 0
 

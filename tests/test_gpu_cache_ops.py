@@ -117,19 +117,19 @@ def test_prefix_attn_against_fp64(ic, case):
         v[b, lens[b]:] = INF
     own = (k, v, lens) if S else (None, None, None)
     at = torch.arange(S, device="cuda")
-    results = []
-    for ws in (None, torch.empty(0, dtype=torch.uint8, device="cuda")):
-        out, lse = ic.prefix_attn(q, kp, vp, *own, ws=ws)
-        ok(ic)
-        results.append(out)
-        for b in sorted({0, 1 % B, B // 2, B - 1}):
-            n = int(lens[b])
-            i = torch.arange(Lq, device="cuda")
-            seen = torch.cat([torch.ones(Lq, P, dtype=torch.bool, device="cuda"),
-                              (at[None] <= n - Lq + i[:, None]) & (at[None] < n)], 1)
-            keys, vals = torch.cat([kp, k[b]]), torch.cat([vp, v[b]])
-            keys = torch.where(seen.any(0)[:, None, None], keys, 0)
-            check_attn(out[b], lse[b], q[b], keys, vals, seen)
+    # a workspace that held anything
+    n = ic.prefix_attn_workspace_bytes(B, Lq, P, S, Hq, Hkv, d)
+    ws = torch.full((max(n, 1),), 255, dtype=torch.uint8, device="cuda")
+    out, lse = ic.prefix_attn(q, kp, vp, *own, ws=ws)
+    ok(ic)
+    i = torch.arange(Lq, device="cuda")
+    for b in sorted({0, 1 % B, B // 2, B - 1}):
+        n = int(lens[b])
+        seen = torch.cat([torch.ones(Lq, P, dtype=torch.bool, device="cuda"),
+                          (at[None] <= n - Lq + i[:, None]) & (at[None] < n)], 1)
+        keys, vals = torch.cat([kp, k[b]]), torch.cat([vp, v[b]])
+        keys = torch.where(seen.any(0)[:, None, None], keys, 0)
+        check_attn(out[b], lse[b], q[b], keys, vals, seen)
 
 
 def test_prefix_attn_rows_that_see_nothing(ic):
@@ -185,6 +185,10 @@ def test_prefix_attn_equals_itself_and_flags_lengths(ic):
     out, lse = ic.prefix_attn(q[7:8], kp, vp)
     ok(ic)
     assert (c[1][7] - lse[0]).abs().max() <= 1e-5                   # clamped to none
+    need = ic.prefix_attn_workspace_bytes(40, 1, 3001, 100, 16, 1, 128)
+    assert need > 0
+    with pytest.raises(ic.IndexCacheError, match="WORKSPACE_TOO_SMALL"):
+        ic.prefix_attn(q, kp, vp, k, v, ws=torch.empty(need - 4, dtype=torch.uint8, device="cuda"))
 
 
 MASS = [
