@@ -3,74 +3,367 @@
 // with lse the natural-log normaliser an attention call returned for the row.
 // Dense: every position the causal rule lets a row see.  Sparse: the
 // positions of an index cache.
+//
+// Dense kernel.  The score tile is computed transposed, keys x rows: a key is
+// a TMEM lane, so a thread adds up its key's weights over the columns with
+// no exchange between threads, in a fixed order (the same bits every run), and
+// masked keys (which may hold anything) touch no other key's sum.  A CTA takes
+// `group` 128-key tiles of one sequence and walks over the row tiles (IPT
+// queries x G heads <= 128 columns) that see them, per K/V head.  Two CTAs
+// share an SM.
+//   warp 0      TMA of K tiles and row tiles into two rings; its lanes also
+//               write each row tile's columns: lse * log2 e (+inf for columns
+//               without a row, whose weight is then 0) and the number of
+//               positions each column sees.  A single row tile stays resident.
+//   warp 1      TMEM allocation and MMA: S^T = K Q^T (M=128 keys, N columns)
+//               into one of two 128-column buffers.
+//   warps 2-9   two warpgroups, one per buffer: thread = key.  p = 2^(scale
+//               log2e S - lse2), summed per tile in four fp32 chains and
+//               across tiles with compensation.
+// When one sequence has few key tiles and many rows, a cluster of up to 8 CTAs
+// shares a key tile: rank r takes every C-th row tile and rank 0 adds the sums
+// through distributed shared memory, in rank order.
 #pragma once
 
 #include "common.cuh"
+#include "dense_attn.cuh"
 #include "prefix_attn.cuh"
 
 namespace ic {
 
+constexpr int AM_THREADS = 320;
+constexpr int AM_TILE = 128;                 // keys per tile, columns per row tile at most
+constexpr int AM_SMEM = 233472 / 2 - 1024;   // two CTAs and their reserved 1 KB fit an SM
+constexpr uint32_t AM_TMEM_COLS = 256;
+
 struct AttnMassArgs {
-    const __nv_bfloat16* q;     // [B, Lq, Hq, D]
-    const __nv_bfloat16* k;     // [B, Lk, Hkv, D]
     const float* lse;           // [B, Lq, Hq]
     const int32_t* lens;        // [B] or null
     float* mass;                // [B, Lk]
-    int B, Lq, Lk, Hq, Hkv, q_offset;
+    int B, Lq, Lk, Hq, Hkv, G, q_offset;
+    int ipt, n_cols;            // queries per row tile; columns of the MMA (a multiple of 16)
+    int row_tiles;              // row tiles of a sequence and K/V head
+    int group;                  // key tiles a CTA (1 when a cluster shares a key tile)
+    int q_stages, k_stages;     // ring depths; one row tile in all: q_stages == 1, loaded once
+    int q_half;                 // bytes of a row tile's 64-column half: n_cols rows of 128
     float scale_log2;
 };
 
-// Positions row i of sequence b sees: [0, returned value).
+// Positions that row i of a sequence of n positions sees: [0, returned value).
 __device__ __forceinline__ int mass_limit(const AttnMassArgs& a, int n, int i) {
     const long long t1 = (a.lens ? (long long)n - a.Lq : (long long)a.q_offset) + i + 1;
     return (int)max(0LL, min(t1, (long long)n));
 }
 
-// Thread = key: its K row in registers, the query rows in shared memory 32 at
-// a time.
 template <int D>
-__global__ void __launch_bounds__(128)
-attn_mass_kernel(const AttnMassArgs a) {
-    __shared__ float sq[32][D], sl[32];
-    __shared__ int lim[32];
-    const int b = blockIdx.y;
-    const long long s = (long long)blockIdx.x * 128 + threadIdx.x;
+struct MassSmem {
+    static constexpr int K_BYTES = AM_TILE * D * 2;
+    static constexpr int MAX_STAGES = 8;
+    // after the tiles: column info of 2 stages, a warpgroup's sums, barriers
+    static constexpr int COLS = 0;                            // [2][lse2 128, limit 128, min limit + pad]
+    static constexpr int COL_STAGE = 2 * AM_TILE * 4 + 16;
+    static constexpr int RED = COLS + 2 * COL_STAGE;          // [128] f32
+    static constexpr int BARS = RED + AM_TILE * 4;
+    static constexpr int N_BARS = 2 * MAX_STAGES + 2 * 2 + 2 * 2 + 1;
+    static constexpr int SLOT = BARS + N_BARS * 8;
+    static constexpr int TAIL = (SLOT + 16 + 15) / 16 * 16;
+};
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// As tmem_ld_wait over 32 registers: no use of r moves ahead of the wait.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            int y, int z, int w, int v) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// tmap_q: {D, G, Hkv, Lq, B}, box {64, G, 1, ipt, 1}; tmap_k: {D, Hkv, Lk, B},
+// box {64, 1, 128, 1}; what lies outside reads as zeros.  Grid: cluster ranks x
+// key groups x B.
+template <int D>
+__global__ void __launch_bounds__(AM_THREADS, 2)
+attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                 const AttnMassArgs a) {
+    using S = MassSmem<D>;
+    extern __shared__ uint8_t am_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x, C = gridDim.x, b = blockIdx.z;
     const int n = seq_len(a.lens, b, a.Lk);
-    const int G = a.Hq / a.Hkv;
-    float total = 0.0f;
-    for (int j = 0; j < a.Hkv; ++j) {
-        uint32_t kr[D / 2];
-        for (int e = 0; e < D / 2; ++e)
-            kr[e] = s < n ? reinterpret_cast<const uint32_t*>(a.k + (((long long)b * a.Lk + s) * a.Hkv + j) * D)[e] : 0u;
-        const long long rows = (long long)a.Lq * G;
-        for (long long r0 = 0; r0 < rows; r0 += 32) {
-            __syncthreads();
-            for (int e = threadIdx.x; e < 32 * D; e += 128) {
-                const long long r = r0 + e / D;
-                const long long row = ((long long)b * a.Lq + r / G) * a.Hq + j * G + r % G;
-                sq[e / D][e % D] = r < rows ? __bfloat162float(a.q[row * D + e % D]) * a.scale_log2 : 0.0f;
-                if (e % D == 0) {
-                    const float l = r < rows ? a.lse[row] : -INFINITY;
-                    sl[e / D] = l * LOG2E;
-                    lim[e / D] = r < rows && l != -INFINITY ? mass_limit(a, n, (int)(r / G)) : 0;
+    const int kt0 = blockIdx.y * a.group;
+    const int kt1 = min(kt0 + a.group, (n + AM_TILE - 1) / AM_TILE);
+    // first row that sees key 0 of a tile: t = base + i >= key
+    const long long base = a.lens ? (long long)n - a.Lq : (long long)a.q_offset;
+    auto first_tile = [&](int kt) {
+        return (int)(min((long long)a.Lq, max(0LL, (long long)kt * AM_TILE - base)) / a.ipt);
+    };
+    // steps of key tile kt: for each K/V head, row tiles first_tile + rank, + C, ...
+    auto rows_of = [&](int kt) {
+        const long long f = min((long long)a.Lq, max(0LL, (long long)kt * AM_TILE - base));
+        const int f0 = (int)(f / a.ipt);
+        return f >= a.Lq || f0 + rank >= a.row_tiles ? 0 : (a.row_tiles - f0 - rank + C - 1) / C;
+    };
+    if (kt0 >= kt1) return;                                     // uniform over the cluster
+    const int q_bytes = a.q_half * (D / 64);
+    const int stage_bytes = a.q_stages * q_bytes + a.k_stages * S::K_BYTES;
+    uint8_t* smem = align_smem_1024(am_raw, (uint32_t)(stage_bytes + S::TAIL));
+    const bool resident = a.q_stages == 1;
+    if (smem != nullptr) {
+        uint8_t* sq = smem;
+        uint8_t* sk = smem + a.q_stages * q_bytes;
+        uint8_t* tail = smem + stage_bytes;
+        float* red = reinterpret_cast<float*>(tail + S::RED);
+        uint64_t* bars = reinterpret_cast<uint64_t*>(tail + S::BARS);
+        uint64_t* k_full = bars;                                // [k_stages]
+        uint64_t* k_empty = bars + S::MAX_STAGES;
+        uint64_t* q_full = bars + 2 * S::MAX_STAGES;            // [q_stages]
+        uint64_t* q_empty = q_full + 2;
+        uint64_t* s_full = q_empty + 2;                         // [2]
+        uint64_t* s_empty = s_full + 2;
+        uint64_t* mma_done = s_empty + 2;
+        uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + S::SLOT);
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < a.k_stages; ++i) {
+                mbar_init(&k_full[i], 1);
+                mbar_init(&k_empty[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&q_full[i], 1 + 32);                  // the copy and the lanes' column info
+                mbar_init(&q_empty[i], 1 + 4);                  // the MMA and a warpgroup's warps
+                mbar_init(&s_full[i], 1);
+                mbar_init(&s_empty[i], 4);
+            }
+            mbar_init(mma_done, 1);
+            fence_barrier_init();
+        }
+        // columns past the row tile's last stay zero: their score is 0, their weight 2^-inf
+        for (int e = threadIdx.x; e < a.q_stages * q_bytes / 16; e += AM_THREADS)
+            reinterpret_cast<uint4*>(sq)[e] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        if (warp == 1) {
+            tmem_alloc(tmem_slot, AM_TMEM_COLS);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        const uint32_t tmem = *tmem_slot;
+
+        if (warp == 0) {
+            int kn = 0, qn = 0;                                 // K tiles and row tiles loaded so far
+            bool ok = true;
+            for (int kt = kt0; kt < kt1 && ok; ++kt) {
+                const int nr = rows_of(kt), f0 = first_tile(kt);
+                for (int j = 0; j < a.Hkv && ok; ++j) {
+                    if (nr == 0) break;
+                    if (kn >= a.k_stages)
+                        ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[kn % a.k_stages], ((kn / a.k_stages) & 1) ^ 1));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const int st = kn % a.k_stages;
+                        mbar_arrive_expect_tx(&k_full[st], (uint32_t)S::K_BYTES);
+                        for (int kb = 0; kb < D / 64; ++kb)
+                            tma_load_4d(sk + st * S::K_BYTES + kb * AM_TILE * 128, &tmap_k, &k_full[st], kb * 64, j,
+                                        kt * AM_TILE, b);
+                    }
+                    ++kn;
+                    for (int x = 0; x < nr; ++x) {
+                        if (resident && qn > 0) break;
+                        const int st = qn & 1, rt = f0 + rank + x * C;
+                        if (qn >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[st], ((qn >> 1) & 1) ^ 1));
+                        if (!ok) break;
+                        if (lane == 0) {
+                            const uint32_t half = (uint32_t)(a.ipt * a.G * 128);
+                            mbar_arrive_expect_tx(&q_full[st], half * (D / 64));
+                            for (int kb = 0; kb < D / 64; ++kb)
+                                tma_load_5d(sq + st * q_bytes + kb * a.q_half, &tmap_q, &q_full[st], kb * 64, 0, j,
+                                            rt * a.ipt, b);
+                        }
+                        // columns c = (query, head) of the row tile
+                        float* cl = reinterpret_cast<float*>(tail + S::COLS + st * S::COL_STAGE);
+                        int* lim = reinterpret_cast<int*>(cl + AM_TILE);
+                        int least = 0x7fffffff;
+                        for (int c = lane; c < AM_TILE; c += 32) {
+                            const int i = rt * a.ipt + c / a.G;
+                            float l2 = INFINITY;
+                            int v = 0;
+                            if (c < a.ipt * a.G && i < a.Lq) {
+                                const float l = __ldg(a.lse + ((long long)b * a.Lq + i) * a.Hq + j * a.G + c % a.G);
+                                if (l != -INFINITY) {           // a row without keys adds nothing
+                                    l2 = l * LOG2E;
+                                    v = mass_limit(a, n, i);
+                                }
+                                least = min(least, v);
+                            }
+                            cl[c] = l2;
+                            lim[c] = v;
+                        }
+#pragma unroll
+                        for (int o = 16; o >= 1; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+                        if (lane == 0) lim[AM_TILE] = least;
+                        __syncwarp();
+                        mbar_arrive(&q_full[st]);
+                        ++qn;
+                    }
                 }
             }
-            __syncthreads();
-            float part = 0.0f;
-            for (int r = 0; r < 32; ++r) {
-                if (s >= lim[r]) continue;
-                float z = 0.0f;
-                for (int e = 0; e < D / 2; ++e) {
-                    const float2 kv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&kr[e]));
-                    z = fmaf(kv.x, sq[r][2 * e], z);
-                    z = fmaf(kv.y, sq[r][2 * e + 1], z);
-                }
-                part += exp2f(z - sl[r]);
+            if (lane == 0) {                                    // never leave with copies in flight
+                for (int c = max(0, kn - a.k_stages); c < kn; ++c)
+                    mbar_wait(&k_full[c % a.k_stages], (c / a.k_stages) & 1);
+                for (int c = max(0, qn - 2); c < qn; ++c) mbar_wait(&q_full[c & 1], (c >> 1) & 1);
             }
-            total += part;
+        } else if (warp == 1) {
+            if (lane == 0) {
+                const uint32_t idesc = idesc_bf16_f32(128, a.n_cols);
+                int kn = 0, step = 0;
+                bool ok = true;
+                for (int kt = kt0; kt < kt1 && ok; ++kt) {
+                    const int nr = rows_of(kt);
+                    for (int j = 0; j < a.Hkv && ok && nr > 0; ++j, ++kn) {
+                        const int ks = kn % a.k_stages;
+                        if (!(ok = mbar_wait(&k_full[ks], (kn / a.k_stages) & 1))) break;
+                        const uint32_t ka = sw128_desc_lo(smem_u32(sk + ks * S::K_BYTES), 16);
+                        for (int x = 0; x < nr; ++x, ++step) {
+                            const int qs = resident ? 0 : step & 1, buf = step & 1;
+                            if (!(ok = mbar_wait(&q_full[qs], resident ? 0 : (step >> 1) & 1))) break;
+                            if (step >= 2 && !(ok = mbar_wait(&s_empty[buf], ((step >> 1) & 1) ^ 1))) break;
+                            tc_fence_after();
+                            const uint32_t qa = sw128_desc_lo(smem_u32(sq + qs * q_bytes), 16);
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t o = (uint32_t)((kk & 3) * 32) >> 4;
+                                tc_mma_ss(tmem + (uint32_t)(buf * AM_TILE),
+                                          ka + o + (uint32_t)((kk >> 2) * AM_TILE * 128 >> 4),
+                                          qa + o + (uint32_t)((kk >> 2) * a.q_half) / 16, idesc, kk > 0 ? 1u : 0u);
+                            }
+                            tc_commit(&s_full[buf]);
+                            if (!resident) tc_commit(&q_empty[qs]);
+                        }
+                        if (ok) tc_commit(&k_empty[ks]);
+                    }
+                }
+                // the MMAs this thread issued are done before TMEM is freed
+                tc_commit(mma_done);
+                mbar_wait(mma_done, 0);
+            }
+        } else {
+            const int g = warp >= 6 ? 1 : 0;                    // warpgroup = buffer
+            const int tr = (warp & 3) * 32 + lane;              // key of the tile = TMEM lane
+            const uint32_t sb = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(g * AM_TILE);
+            const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+            const int chunks = a.n_cols / 16;
+            int step = 0;
+            bool ok = true;
+            for (int kt = kt0; kt < kt1; ++kt) {                // a failed wait ends the work, not the barriers
+                const int steps = rows_of(kt) * a.Hkv;
+                const int key = kt * AM_TILE + tr;
+                float total = 0.0f, comp = 0.0f;                // compensated sum over the row tiles
+                for (int x = 0; x < steps && ok; ++x, ++step) {
+                    if ((step & 1) != g) continue;
+                    const int qs = resident ? 0 : step & 1;
+                    // the row tile's column info, then its scores
+                    if (!__all_sync(0xffffffffu, mbar_wait(&q_full[qs], resident ? 0 : (step >> 1) & 1)) ||
+                        !__all_sync(0xffffffffu, mbar_wait(&s_full[g], (step >> 1) & 1))) { ok = false; break; }
+                    tc_fence_after();
+                    const float* cl = reinterpret_cast<const float*>(tail + S::COLS + qs * S::COL_STAGE);
+                    const int* lim = reinterpret_cast<const int*>(cl + AM_TILE);
+                    const bool masked = lim[AM_TILE] < (kt + 1) * AM_TILE;
+                    float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                    uint32_t v[2][16];
+                    auto add = [&](uint32_t (&s)[16], int c) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 l = *reinterpret_cast<const float4*>(cl + c * 16 + e);
+                            const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
+                                                         sc2, make_float2(-l.x, -l.y));
+                            const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])),
+                                                         sc2, make_float2(-l.z, -l.w));
+                            float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
+                            float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+                            if (masked) {
+                                const int4 m = *reinterpret_cast<const int4*>(lim + c * 16 + e);
+                                p0.x = key < m.x ? p0.x : 0.0f;
+                                p0.y = key < m.y ? p0.y : 0.0f;
+                                p1.x = key < m.z ? p1.x : 0.0f;
+                                p1.y = key < m.w ? p1.y : 0.0f;
+                            }
+                            acc[0] = __fadd2_rn(acc[0], p0);
+                            acc[1] = __fadd2_rn(acc[1], p1);
+                        }
+                    };
+                    tmem_ld_32x32b_x16(sb, v[0]);
+                    for (int c = 0; c < chunks; c += 2) {
+                        tmem_ld_wait(v[0]);
+                        if (c + 1 < chunks) tmem_ld_32x32b_x16(sb + (c + 1) * 16, v[1]);
+                        add(v[0], c);
+                        if (c + 1 < chunks) {
+                            tmem_ld_wait(v[1]);
+                            if (c + 2 < chunks) tmem_ld_32x32b_x16(sb + (c + 2) * 16, v[0]);
+                            add(v[1], c + 1);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&s_empty[g]);
+                        if (!resident) mbar_arrive(&q_empty[qs]);
+                    }
+                    const float2 s2 = __fadd2_rn(acc[0], acc[1]);
+                    const float y = (s2.x + s2.y) - comp;
+                    const float t = total + y;
+                    comp = (t - total) - y;
+                    total = t;
+                }
+                if (C > 1 || steps > 1) {
+                    // both warpgroups hold a share of the tile's keys
+                    if (g == 1) red[tr] = total;
+                    named_bar(1, 256);
+                    if (g == 0) {
+                        total += red[tr];
+                        if (C > 1) red[tr] = total;
+                        else if (key < n) a.mass[(long long)b * a.Lk + key] += total;
+                    }
+                    named_bar(1, 256);
+                } else if (steps == 1 && ((step - 1) & 1) == g && key < n) {
+                    a.mass[(long long)b * a.Lk + key] += total;
+                }
+            }
+        }
+        tc_fence_before();
+        __syncthreads();
+        if (warp == 1) {
+            tc_fence_after();
+            tmem_dealloc(tmem, AM_TMEM_COLS);
+        }
+        if (C > 1) {
+            // rank 0 adds the ranks' sums of the one key tile in rank order
+            cluster_sync();
+            const int key = kt0 * AM_TILE + (int)threadIdx.x;
+            if (rank == 0 && threadIdx.x < AM_TILE && key < n) {
+                float total = red[threadIdx.x];
+                for (int r = 1; r < C; ++r) total += ld_dsmem_f32(smem_u32(red + threadIdx.x), (uint32_t)r);
+                a.mass[(long long)b * a.Lk + key] += total;
+            }
+            cluster_sync();               // no CTA leaves while rank 0 may read its shared memory
         }
     }
-    if (s < n) a.mass[(long long)b * a.Lk + s] += total;
 }
 
 struct SparseMassArgs {

@@ -54,20 +54,6 @@ __device__ __forceinline__ uint32_t ev_key(float f) {
     return f != f ? score_key(-INFINITY) : score_key(f);
 }
 
-__device__ __forceinline__ void ev_cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint4 ev_ld_cluster_v4(uint32_t local_addr, uint32_t rank) {
-    uint32_t remote;
-    uint4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_addr), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(remote)
-                 : "memory");
-    return v;
-}
-
 __global__ void __launch_bounds__(EV_THREADS)
 evict_select_kernel(const EvictArgs a) {
     using S = EvictSmem;
@@ -137,12 +123,12 @@ evict_select_kernel(const EvictArgs a) {
                 }
             }
         }
-        ev_cluster_sync();
+        cluster_sync();
         // every CTA sums all slices' bins, highest first: thread t has bins [2044 - 4t, 2048 - 4t)
         uint32_t c[4] = {0, 0, 0, 0};
         const int bin0 = EV_BINS - 4 - 4 * tid;
         for (int r = 0; r < C; ++r) {
-            const uint4 v = ev_ld_cluster_v4(smem_u32(h + bin0), (uint32_t)r);
+            const uint4 v = ld_dsmem_v4(smem_u32(h + bin0), (uint32_t)r);
             c[0] += v.w;
             c[1] += v.z;
             c[2] += v.y;
@@ -205,10 +191,10 @@ evict_select_kernel(const EvictArgs a) {
         cnt[0] = g;
         cnt[1] = q;
     }
-    ev_cluster_sync();
+    cluster_sync();
     uint32_t gt_before = 0, eq_before = 0;
     for (int r = 0; r < rank; ++r) {
-        const uint4 v = ev_ld_cluster_v4(smem_u32(cnt), (uint32_t)r);
+        const uint4 v = ld_dsmem_v4(smem_u32(cnt), (uint32_t)r);
         gt_before += v.x;
         eq_before += v.y;
     }
@@ -231,7 +217,7 @@ evict_select_kernel(const EvictArgs a) {
         gt_before += (uint32_t)__popc(mg);
         eq_before += (uint32_t)__popc(me);
     }
-    ev_cluster_sync();                       // no CTA leaves while another may read its shared memory
+    cluster_sync();                       // no CTA leaves while another may read its shared memory
 }
 
 // ---------------------------------------------------------------- compaction

@@ -25,6 +25,40 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// Launch shape of the dense accumulated weights.
+struct MassGeom {
+    int G, ipt, n_cols, row_tiles, key_tiles, group, ranks, q_stages, k_stages;
+    size_t smem;
+};
+
+MassGeom mass_geom(int B, int Lq, int Lk, int Hq, int Hkv, int d, int sms) {
+    MassGeom g;
+    const int T = ic::AM_TILE;
+    g.G = Hq / Hkv;
+    g.ipt = std::min(T / g.G, Lq);
+    g.n_cols = (g.ipt * g.G + 15) / 16 * 16;
+    g.row_tiles = (Lq + g.ipt - 1) / g.ipt;
+    g.key_tiles = (Lk + T - 1) / T;
+    const long long tiles = (long long)B * g.key_tiles;
+    const long long steps = (long long)g.row_tiles * Hkv;          // of a key tile that every row sees
+    const long long slots = 2LL * sms;                             // CTAs at once
+    // few key tiles: up to 8 CTAs share one, with at least 4 row tiles each
+    g.ranks = 1;
+    while (g.ranks < 8 && tiles * g.ranks < 2 * slots && g.row_tiles / (2 * g.ranks) >= 4) g.ranks *= 2;
+    // many: CTAs of about 8 steps, as long as they fill the GPU four times
+    long long group = g.ranks > 1 ? 1 : std::min((7 + steps) / steps, tiles / (4 * slots));
+    group = std::max(group, (g.key_tiles + 65534LL) / 65535);
+    g.group = (int)std::max(1LL, std::min<long long>(group, g.key_tiles));
+    if (g.group > 1) g.ranks = 1;
+    g.q_stages = steps == 1 ? 1 : 2;
+    const int k_bytes = T * d * 2, q_bytes = g.n_cols * d * 2;
+    const int tail = d == 64 ? ic::MassSmem<64>::TAIL : ic::MassSmem<128>::TAIL;
+    const int room = ic::AM_SMEM - 1024 - tail - g.q_stages * q_bytes;
+    g.k_stages = std::max(1, std::min({room / k_bytes, 8, g.group * Hkv}));
+    g.smem = (size_t)g.q_stages * q_bytes + (size_t)g.k_stages * k_bytes + tail + 1024;
+    return g;
+}
+
 // CTAs per sequence of the eviction select: enough that a slice fits in
 // shared memory, and about 4K positions each for short caches.
 int evict_cluster(int Lk) {
@@ -224,22 +258,50 @@ int ic_attn_mass(const uint16_t* q, const uint16_t* k, const float* lse, const i
         return fail(IC_ERR_UNSUPPORTED, "q and k must be 16-byte aligned");
     if (!aligned4(lse) || !aligned4(lens) || !aligned4(mass))
         return fail(IC_ERR_UNSUPPORTED, "lse, lens and mass must be 4-byte aligned");
-    if (B > 65535) return fail(IC_ERR_UNSUPPORTED, "B=%d too large", B);
+    if (B > 65535 || Lk > (1 << 30) || (long long)Lq * Hq > MAX_GRID_X)
+        return fail(IC_ERR_UNSUPPORTED, "B=%d Lq=%d Lk=%d (supported: B <= 65535, Lk <= 2^30, Lq*Hq < 2^31)",
+                    B, Lq, Lk);
     int dev, sms;
     if ((rc = device_setup(&dev, &sms))) return rc;
+    const MassGeom g = mass_geom(B, Lq, Lk, Hq, Hkv, d, sms);
+    CUtensorMap tq, tk;
+    const uint64_t hd = (uint64_t)Hkv * d, qd = (uint64_t)Hq * d;
+    {
+        const uint64_t dims[5] = {(uint64_t)d, (uint64_t)g.G, (uint64_t)Hkv, (uint64_t)Lq, (uint64_t)B};
+        const uint64_t strides[4] = {(uint64_t)d * 2, (uint64_t)g.G * d * 2, qd * 2, qd * 2 * Lq};
+        const uint32_t box[5] = {64, (uint32_t)g.G, 1, (uint32_t)g.ipt, 1};
+        if ((rc = make_tmap(&tq, q, 5, dims, strides, box))) return rc;
+    }
+    {
+        const uint64_t dims[4] = {(uint64_t)d, (uint64_t)Hkv, (uint64_t)Lk, (uint64_t)B};
+        const uint64_t strides[3] = {(uint64_t)d * 2, hd * 2, hd * 2 * Lk};
+        const uint32_t box[4] = {64, 1, ic::AM_TILE, 1};
+        if ((rc = make_tmap(&tk, k, 4, dims, strides, box))) return rc;
+    }
     ic::AttnMassArgs a{};
-    a.q = reinterpret_cast<const __nv_bfloat16*>(q);
-    a.k = reinterpret_cast<const __nv_bfloat16*>(k);
     a.lse = lse;
     a.lens = lens;
     a.mass = mass;
-    a.B = B; a.Lq = Lq; a.Lk = Lk; a.Hq = Hq; a.Hkv = Hkv; a.q_offset = q_offset;
+    a.B = B; a.Lq = Lq; a.Lk = Lk; a.Hq = Hq; a.Hkv = Hkv; a.G = g.G; a.q_offset = q_offset;
+    a.ipt = g.ipt; a.n_cols = g.n_cols; a.row_tiles = g.row_tiles; a.group = g.group;
+    a.q_stages = g.q_stages; a.k_stages = g.k_stages; a.q_half = g.n_cols * 128;
     a.scale_log2 = scale_log2_of(scale, d);
-    const dim3 grid((unsigned)((Lk + 127LL) / 128), (unsigned)B);
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (d == 64) ic::attn_mass_kernel<64><<<grid, 128, 0, st>>>(a);
-    else ic::attn_mass_kernel<128><<<grid, 128, 0, st>>>(a);
-    return launched(cudaGetLastError(), "attn_mass launch");
+    const int groups = (g.key_tiles + g.group - 1) / g.group;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)g.ranks, (unsigned)groups, (unsigned)B);
+    cfg.blockDim = dim3(ic::AM_THREADS);
+    cfg.dynamicSmemBytes = g.smem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)g.ranks;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaError_t e = d == 64 ? cudaLaunchKernelEx(&cfg, ic::attn_mass_kernel<64>, tq, tk, a)
+                            : cudaLaunchKernelEx(&cfg, ic::attn_mass_kernel<128>, tq, tk, a);
+    return launched(e, "attn_mass launch");
 }
 
 size_t ic_attn_mass_sparse_workspace_bytes(int B, int Lq, int Lk) {

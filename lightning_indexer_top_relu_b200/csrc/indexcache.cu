@@ -808,6 +808,10 @@ int device_setup(int* dev_out, int* sms_out) {
                              ic::PrefixSmem<64>::ALLOC);
         cudaFuncSetAttribute(ic::prefix_attn_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ic::PrefixSmem<128>::ALLOC);
+        cudaFuncSetAttribute(ic::attn_mass_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ic::AM_SMEM);
+        cudaFuncSetAttribute(ic::attn_mass_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ic::AM_SMEM);
         cudaFuncSetAttribute(ic::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ic::EvictSmem::bytes(ic::EV_CACHE_MAX));
         e = cudaGetLastError();
