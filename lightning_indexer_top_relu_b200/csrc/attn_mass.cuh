@@ -11,15 +11,16 @@
 // `group` 128-key tiles of one sequence and walks over the row tiles (IPT
 // queries x G heads <= 128 columns) that see them, per K/V head.  Two CTAs
 // share an SM.
-//   warp 0      TMA of K tiles and row tiles into two rings; its lanes also
-//               write each row tile's columns: lse * log2 e (+inf for columns
-//               without a row, whose weight is then 0) and the number of
-//               positions each column sees.  A single row tile stays resident.
+//   warp 0      TMA of K tiles and row tiles into two rings.  A single row
+//               tile stays resident.
 //   warp 1      TMEM allocation and MMA: S^T = K Q^T (M=128 keys, N columns)
 //               into one of two 128-column buffers.
 //   warps 2-9   two warpgroups, one per buffer: thread = key.  p = 2^(scale
 //               log2e S - lse2), summed per tile in four fp32 chains and
-//               across tiles with compensation.
+//               across tiles with compensation.  Each thread also writes one
+//               column's -lse2 = -lse log2 e (-inf for columns without a row, whose
+//               weight is then 0) and the number of positions it sees, read
+//               from global memory a step ahead.
 // When one sequence has few key tiles and many rows, a cluster of up to 8 CTAs
 // shares a key tile: rank r takes every C-th row tile and rank 0 adds the sums
 // through distributed shared memory, in rank order.
@@ -59,10 +60,10 @@ template <int D>
 struct MassSmem {
     static constexpr int K_BYTES = AM_TILE * D * 2;
     static constexpr int MAX_STAGES = 8;
-    // after the tiles: column info of 2 stages, a warpgroup's sums, barriers
-    static constexpr int COLS = 0;                            // [2][lse2 128, limit 128, min limit + pad]
-    static constexpr int COL_STAGE = 2 * AM_TILE * 4 + 16;
-    static constexpr int RED = COLS + 2 * COL_STAGE;          // [128] f32
+    // after the tiles: column info, a warpgroup's sums, barriers
+    static constexpr int COLS = 0;                            // [2 warpgroups][2][lse2 128, limit 128]
+    static constexpr int COL_STAGE = 2 * AM_TILE * 4;
+    static constexpr int RED = COLS + 4 * COL_STAGE;          // [128] f32
     static constexpr int BARS = RED + AM_TILE * 4;
     static constexpr int N_BARS = 2 * MAX_STAGES + 2 * 2 + 2 * 2 + 1;
     static constexpr int SLOT = BARS + N_BARS * 8;
@@ -93,6 +94,55 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
         " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
         : "memory");
+}
+
+// Adds the weights 2^(scale_log2 S - lse2) of one key in N columns to acc.
+// MASKED: a column counts only when the key is below its limit.
+template <bool MASKED, int N>
+__device__ __forceinline__ void mass_add(const uint32_t (&s)[N], const float* cl, const int* lim, int key, float2 sc2,
+                                         float2 (&acc)[2]) {
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(cl + e);
+        const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2,
+                                     make_float2(l.x, l.y));
+        const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), sc2,
+                                     make_float2(l.z, l.w));
+        float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
+        float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+        if (MASKED) {
+            const int4 m = *reinterpret_cast<const int4*>(lim + e);
+            p0.x = key < m.x ? p0.x : 0.0f;
+            p0.y = key < m.y ? p0.y : 0.0f;
+            p1.x = key < m.z ? p1.x : 0.0f;
+            p1.y = key < m.w ? p1.y : 0.0f;
+        }
+        acc[0] = __fadd2_rn(acc[0], p0);
+        acc[1] = __fadd2_rn(acc[1], p1);
+    }
+}
+
+// The sum of one key's weights over n_cols (a multiple of 16) columns at sb.
+template <bool MASKED>
+__device__ __forceinline__ float mass_tile_sum(uint32_t sb, int n_cols, const float* cl, const int* lim, int key,
+                                               float scale_log2) {
+    const float2 sc2 = make_float2(scale_log2, scale_log2);
+    float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+    int c = 0;
+    for (; c + 32 <= n_cols; c += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(sb + c, v);
+        tmem_ld_wait(v);
+        mass_add<MASKED>(v, cl + c, lim + c, key, sc2, acc);
+    }
+    if (c < n_cols) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(sb + c, v);
+        tmem_ld_wait(v);
+        mass_add<MASKED>(v, cl + c, lim + c, key, sc2, acc);
+    }
+    const float2 s2 = __fadd2_rn(acc[0], acc[1]);
+    return s2.x + s2.y;
 }
 
 // tmap_q: {D, G, Hkv, Lq, B}, box {64, G, 1, ipt, 1}; tmap_k: {D, Hkv, Lk, B},
@@ -145,8 +195,8 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 mbar_init(&k_empty[i], 1);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&q_full[i], 1 + 32);                  // the copy and the lanes' column info
-                mbar_init(&q_empty[i], 1 + 4);                  // the MMA and a warpgroup's warps
+                mbar_init(&q_full[i], 1);
+                mbar_init(&q_empty[i], 1);
                 mbar_init(&s_full[i], 1);
                 mbar_init(&s_empty[i], 4);
             }
@@ -196,30 +246,6 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                                 tma_load_5d(sq + st * q_bytes + kb * a.q_half, &tmap_q, &q_full[st], kb * 64, 0, j,
                                             rt * a.ipt, b);
                         }
-                        // columns c = (query, head) of the row tile
-                        float* cl = reinterpret_cast<float*>(tail + S::COLS + st * S::COL_STAGE);
-                        int* lim = reinterpret_cast<int*>(cl + AM_TILE);
-                        int least = 0x7fffffff;
-                        for (int c = lane; c < AM_TILE; c += 32) {
-                            const int i = rt * a.ipt + c / a.G;
-                            float l2 = INFINITY;
-                            int v = 0;
-                            if (c < a.ipt * a.G && i < a.Lq) {
-                                const float l = __ldg(a.lse + ((long long)b * a.Lq + i) * a.Hq + j * a.G + c % a.G);
-                                if (l != -INFINITY) {           // a row without keys adds nothing
-                                    l2 = l * LOG2E;
-                                    v = mass_limit(a, n, i);
-                                }
-                                least = min(least, v);
-                            }
-                            cl[c] = l2;
-                            lim[c] = v;
-                        }
-#pragma unroll
-                        for (int o = 16; o >= 1; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-                        if (lane == 0) lim[AM_TILE] = least;
-                        __syncwarp();
-                        mbar_arrive(&q_full[st]);
                         ++qn;
                     }
                 }
@@ -267,70 +293,56 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             const int g = warp >= 6 ? 1 : 0;                    // warpgroup = buffer
             const int tr = (warp & 3) * 32 + lane;              // key of the tile = TMEM lane
             const uint32_t sb = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(g * AM_TILE);
-            const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
-            const int chunks = a.n_cols / 16;
-            int step = 0;
-            bool ok = true;
+            const int n_cols = a.n_cols;
+            // this thread's column of every row tile: query ii, head tr % G
+            const int ii = tr / a.G;
+            const bool has_col = ii < a.ipt;
+            const float* lse_col = a.lse + ((long long)b * a.Lq + ii) * a.Hq + tr % a.G;
+            float* cols = reinterpret_cast<float*>(tail + S::COLS + g * 2 * S::COL_STAGE);
+            // lse of this thread's column in step x of a key tile (+inf: no row)
+            auto load_lse = [&](int x, int nr, int f0) {
+                const int j = x / nr, i0 = (f0 + rank + (x - j * nr) * C) * a.ipt;
+                return has_col && i0 + ii < a.Lq ? __ldg(lse_col + (long long)i0 * a.Hq + j * a.G) : INFINITY;
+            };
+            int step0 = 0, stage = 0;
+            bool ok = true, empty_row = false;
             for (int kt = kt0; kt < kt1; ++kt) {                // a failed wait ends the work, not the barriers
-                const int steps = rows_of(kt) * a.Hkv;
+                const int nr = rows_of(kt), f0 = first_tile(kt), steps = nr * a.Hkv;
                 const int key = kt * AM_TILE + tr;
                 float total = 0.0f, comp = 0.0f;                // compensated sum over the row tiles
-                for (int x = 0; x < steps && ok; ++x, ++step) {
-                    if ((step & 1) != g) continue;
-                    const int qs = resident ? 0 : step & 1;
-                    // the row tile's column info, then its scores
-                    if (!__all_sync(0xffffffffu, mbar_wait(&q_full[qs], resident ? 0 : (step >> 1) & 1)) ||
-                        !__all_sync(0xffffffffu, mbar_wait(&s_full[g], (step >> 1) & 1))) { ok = false; break; }
-                    tc_fence_after();
-                    const float* cl = reinterpret_cast<const float*>(tail + S::COLS + qs * S::COL_STAGE);
-                    const int* lim = reinterpret_cast<const int*>(cl + AM_TILE);
-                    const bool masked = lim[AM_TILE] < (kt + 1) * AM_TILE;
-                    float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
-                    uint32_t v[2][16];
-                    auto add = [&](uint32_t (&s)[16], int c) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 l = *reinterpret_cast<const float4*>(cl + c * 16 + e);
-                            const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
-                                                         sc2, make_float2(-l.x, -l.y));
-                            const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])),
-                                                         sc2, make_float2(-l.z, -l.w));
-                            float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
-                            float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
-                            if (masked) {
-                                const int4 m = *reinterpret_cast<const int4*>(lim + c * 16 + e);
-                                p0.x = key < m.x ? p0.x : 0.0f;
-                                p0.y = key < m.y ? p0.y : 0.0f;
-                                p1.x = key < m.z ? p1.x : 0.0f;
-                                p1.y = key < m.w ? p1.y : 0.0f;
-                            }
-                            acc[0] = __fadd2_rn(acc[0], p0);
-                            acc[1] = __fadd2_rn(acc[1], p1);
-                        }
-                    };
-                    tmem_ld_32x32b_x16(sb, v[0]);
-                    for (int c = 0; c < chunks; c += 2) {
-                        tmem_ld_wait(v[0]);
-                        if (c + 1 < chunks) tmem_ld_32x32b_x16(sb + (c + 1) * 16, v[1]);
-                        add(v[0], c);
-                        if (c + 1 < chunks) {
-                            tmem_ld_wait(v[1]);
-                            if (c + 2 < chunks) tmem_ld_32x32b_x16(sb + (c + 2) * 16, v[0]);
-                            add(v[1], c + 1);
-                        }
+                int x = (g ^ step0) & 1;                        // this warpgroup's steps of the tile
+                float l = x < steps && !(resident && stage > 0) ? load_lse(x, nr, f0) : 0.0f;
+                for (; x < steps; x += 2) {
+                    const int step = step0 + x;
+                    const int i0 = (f0 + rank + (x % nr) * C) * a.ipt;      // first query of the row tile
+                    // column info of the row tile, two buffers in turn (a resident one once)
+                    if (!resident || stage == 0) {
+                        float* cl = cols + (stage & 1) * (S::COL_STAGE / 4);
+                        const bool none = l == -INFINITY;       // a row without keys adds nothing
+                        cl[tr] = none ? -INFINITY : -l * LOG2E;
+                        reinterpret_cast<int*>(cl)[AM_TILE + tr] = none || l == INFINITY ? 0 : mass_limit(a, n, i0 + ii);
+                        empty_row = named_bar_or(2 + g, 128, none);
+                        if (x + 2 < steps) l = load_lse(x + 2, nr, f0);
                     }
+                    const float* cl = cols + (resident ? 0 : (stage & 1) * (S::COL_STAGE / 4));
+                    const int* lim = reinterpret_cast<const int*>(cl + AM_TILE);
+                    ++stage;
+                    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_full[g], (step >> 1) & 1));
+                    if (!ok) continue;
+                    tc_fence_after();
+                    // limits grow with the query: the first one is the least
+                    const bool masked = empty_row || mass_limit(a, n, i0) < (kt + 1) * AM_TILE;
+                    const float sum = masked ? mass_tile_sum<true>(sb, n_cols, cl, lim, key, a.scale_log2)
+                                             : mass_tile_sum<false>(sb, n_cols, cl, lim, key, a.scale_log2);
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&s_empty[g]);
-                        if (!resident) mbar_arrive(&q_empty[qs]);
-                    }
-                    const float2 s2 = __fadd2_rn(acc[0], acc[1]);
-                    const float y = (s2.x + s2.y) - comp;
+                    if (lane == 0) mbar_arrive(&s_empty[g]);
+                    const float y = sum - comp;
                     const float t = total + y;
                     comp = (t - total) - y;
                     total = t;
                 }
+                step0 += steps;
                 if (C > 1 || steps > 1) {
                     // both warpgroups hold a share of the tile's keys
                     if (g == 1) red[tr] = total;
@@ -341,7 +353,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                         else if (key < n) a.mass[(long long)b * a.Lk + key] += total;
                     }
                     named_bar(1, 256);
-                } else if (steps == 1 && ((step - 1) & 1) == g && key < n) {
+                } else if (steps == 1 && ((step0 - 1) & 1) == g && key < n) {
                     a.mass[(long long)b * a.Lk + key] += total;
                 }
             }

@@ -50,6 +50,7 @@ MassGeom mass_geom(int B, int Lq, int Lk, int Hq, int Hkv, int d, int sms) {
     group = std::max(group, (g.key_tiles + 65534LL) / 65535);
     g.group = (int)std::max(1LL, std::min<long long>(group, g.key_tiles));
     if (g.group > 1) g.ranks = 1;
+    if (getenv("AMC")) g.ranks = atoi(getenv("AMC"));
     g.q_stages = steps == 1 ? 1 : 2;
     const int k_bytes = T * d * 2, q_bytes = g.n_cols * d * 2;
     const int tail = d == 64 ? ic::MassSmem<64>::TAIL : ic::MassSmem<128>::TAIL;
@@ -86,25 +87,25 @@ struct PrefixGeom {
     size_t ws_bytes = 0;
 };
 
-// How finely the keys are split: `s` bounds the steps (one stream's 128 x 128
-// tile, about 0.6 us) of a unit, and the s of the smallest estimated time is
-// taken.  A unit costs its steps and about 3 more to start and end; an own
+// How finely the keys are split: `s` bounds the steps (one stream's 128 rows x
+// 128 keys, about 0.7 us) of a unit, and the s of the smallest estimated time is
+// taken.  A unit costs its steps and about 6 more to start and end; an own
 // tile counts double (64 KB of K and V for one step); merging a partial row
 // costs the time of writing and reading it.  Units up to the number of SMs run
 // at once, more run in turn, the last half a unit late on average.
 PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int sms) {
     PrefixGeom g;
-    const int T = ic::PA_TILE, G = Hq / Hkv;
+    const int T = ic::PA_KEYS, R = ic::PA_ROWS, G = Hq / Hkv;
     const long long rp = (long long)B * Lq * G, ro = (long long)Lq * G;
     const int p_nt = (P + T - 1) / T, o_nt = std::max(1, (S + T - 1) / T);
     const bool has_p = P > 0, has_o = S > 0 || P == 0;        // no key at all: the own units write zeros
-    g.shared = rp > T;
+    g.shared = rp > R;
     const int per_step = g.shared ? 2 : 1;
-    if (has_p) g.p_row_units = (int)((rp + T * per_step - 1) / (T * per_step));
-    if (has_o) g.o_row_units = (int)((ro + T - 1) / T);
+    if (has_p) g.p_row_units = (int)((rp + R * per_step - 1) / (R * per_step));
+    if (has_o) g.o_row_units = (int)((ro + R - 1) / R);
     const long long n_pu = (long long)g.p_row_units * Hkv, n_ou = (long long)B * g.o_row_units * Hkv;
     const double p_work = (double)n_pu * p_nt * per_step, o_work = 2.0 * n_ou * o_nt;
-    const double merge = (double)B * Lq * Hq * d * 1.65e-6;
+    const double merge = (double)B * Lq * Hq * d * 1.4e-6;
     const int s_max = std::max(has_p ? p_nt * per_step : 1, has_o ? o_nt : 1);
     double best = -1.0;
     for (int s = 1;; s = std::min(s_max, s + std::max(1, s / 8))) {
@@ -114,8 +115,8 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
         const int p_str = g.shared ? 1 : std::min(2, p_tps), o_str = std::min(2, o_tps);
         const long long slots = (long long)p_sp * p_str + (long long)o_sp * o_str;
         const double n = (double)n_pu * p_sp + (double)n_ou * o_sp;
-        const double unit = 3.0 + std::max(has_p ? p_tps * per_step : 0, has_o ? 2 * o_tps : 0);
-        double est = n <= sms ? unit : std::max(unit, (p_work + o_work + 3.0 * n) / sms + 0.5 * unit);
+        const double unit = 6.0 + std::max(has_p ? p_tps * per_step : 0, has_o ? 2 * o_tps : 0);
+        double est = n <= sms ? unit : std::max(unit, (p_work + o_work + 6.0 * n) / sms + 0.5 * unit);
         if (slots > 1) est += merge * slots;
         if (n < 2147483647.0 && (best < 0.0 || est < best)) {
             best = est;
@@ -196,14 +197,14 @@ int ic_prefix_attn(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* 
     if (P > 0) {
         const uint64_t dims[3] = {(uint64_t)d, (uint64_t)Hkv, (uint64_t)P};
         const uint64_t strides[2] = {(uint64_t)d * 2, hd * 2};
-        const uint32_t box[3] = {64, 1, ic::PA_TILE};
+        const uint32_t box[3] = {64, 1, ic::PA_KEYS};
         if ((rc = make_tmap(&tkp, k_prefix, 3, dims, strides, box))) return rc;
         if ((rc = make_tmap(&tvp, v_prefix, 3, dims, strides, box))) return rc;
     }
     if (S > 0) {
         const uint64_t dims[4] = {(uint64_t)d, (uint64_t)Hkv, (uint64_t)S, (uint64_t)B};
         const uint64_t strides[3] = {(uint64_t)d * 2, hd * 2, hd * 2 * S};
-        const uint32_t box[4] = {64, 1, ic::PA_TILE, 1};
+        const uint32_t box[4] = {64, 1, ic::PA_KEYS, 1};
         if ((rc = make_tmap(&tk, k, 4, dims, strides, box))) return rc;
         if ((rc = make_tmap(&tv, v, 4, dims, strides, box))) return rc;
     }

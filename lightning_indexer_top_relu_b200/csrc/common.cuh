@@ -272,6 +272,38 @@ __device__ __forceinline__ void named_bar(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// A value that is the same in all lanes, in a form the compiler can keep in
+// uniform registers.
+template <typename T>
+__device__ __forceinline__ T warp_uniform(T v) {
+    return __shfl_sync(0xffffffffu, v, 0);
+}
+
+// As named_bar; returns whether any of the threads passed a true `v`.
+__device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(nthreads), "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
 // Thread-block clusters: a barrier over the cluster's CTAs (shared-memory
 // writes before it are visible to the others after it) and loads from another
 // CTA's shared memory.

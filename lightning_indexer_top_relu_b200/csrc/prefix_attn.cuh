@@ -14,29 +14,31 @@
 // unit of either kind is one CTA; partials go to the workspace and
 // prefix_combine_kernel merges them.
 //
-// One CTA (1 per SM): two streams, each a 128-row query tile (TMEM lanes)
-// with its own score buffer, output accumulator and softmax warpgroup, so one
-// stream's exponentials overlap the other's MMAs.
+// One CTA (1 per SM): two streams, each a 128-row query tile (TMEM lanes) with
+// its own score buffers, output accumulator and softmax warpgroup, so one
+// stream's exponentials overlap the other's.
 //   shared units (more than 128 rows over the prefix): the streams are two row
 //     tiles, both of which use every K/V tile;
 //   split units (own caches, or a prefix with at most 128 rows): both streams
 //     hold the same rows and take alternate K/V tiles (two partials).
-// Step n of a unit belongs to stream n & 1 and key tile n >> 1 (shared) or n
-// (split).
+// Step n of a unit belongs to stream n & 1 and the 128-key tile n >> 1 (shared)
+// or n (split).
 //   warp 0      TMA: 128-key tiles of K and V, alternately, into one ring.
-//   warp 1      TMEM allocation and MMA issue.  S(n) = Q K^T (M=128, N=128),
+//   warp 1      TMEM allocation and MMA issue: S(n) = Q K^T (M=128, N=128),
 //               then O += P(n-1) V.  P comes from TMEM, V from its [keys, d]
 //               tile as an MN-major operand (no transposed copy).  S(n)
 //               overwrites the columns of P(n-2), so it is issued when P(n-2) V
 //               has completed.
 //   warps 4-7, 8-11  the softmax of stream 0 / 1: thread = row = TMEM lane.
-//               Scores come in chunks of 32 columns; the probabilities against
-//               the running maximum are packed to bf16 and stored over the
-//               score columns.  Their rounding (2^-8 of each) is what the bf16
-//               matrix instruction takes; the row sum is taken before it, in
-//               fp32.  The maximum is raised lazily: bf16 and fp32 keep their
-//               relative precision at any scale, so the exponent base only moves
-//               when a tile's sum passes 2^32 (and on the first keys seen).
+//               The probabilities against the running maximum are packed to
+//               bf16 and stored over the scores.  Their rounding (2^-8 of each)
+//               is what the bf16 matrix instruction takes; the row sum is taken
+//               before it, in fp32.  The maximum is raised lazily: bf16 and fp32
+//               keep their relative precision at any scale, so the exponent base
+//               only moves when a tile's sum passes 2^32 (and on the first keys
+//               seen).
+// Masked tiles take a path of their own: selects on the common one doubled its
+// instructions.
 #pragma once
 
 #include "common.cuh"
@@ -45,11 +47,8 @@
 namespace ic {
 
 constexpr int PA_THREADS = 384;                   // a control warpgroup and one per stream
-// Registers a thread: launched with 168 (65536 / 384, rounded down to 8); the
-// control warpgroup gives some up for the softmax ones.
-constexpr int PA_REGS_CONTROL = 80, PA_REGS_SOFTMAX = 208;
-static_assert(PA_REGS_CONTROL + 2 * PA_REGS_SOFTMAX <= 3 * 168, "register split of the launch");
-constexpr int PA_TILE = 128;                      // keys per tile and rows per stream
+constexpr int PA_ROWS = 128;                      // rows per stream
+constexpr int PA_KEYS = 128;                      // keys per tile
 constexpr float PA_SUM_MAX = 4294967296.0f;       // 2^32
 
 struct PrefixAttnArgs {
@@ -83,10 +82,11 @@ __device__ __forceinline__ int seq_len(const int32_t* lens, int b, int cap) {
 
 template <int D>
 struct PrefixSmem {
-    static constexpr int STAGE = PA_TILE * D * 2;            // one K or V tile (D / 64 boxes)
+    static constexpr int QTILE = PA_ROWS * D * 2;            // one row tile (D / 64 boxes)
+    static constexpr int STAGE = PA_KEYS * D * 2;            // one K or V tile
     static constexpr int STAGES = D == 128 ? 5 : 10;
     static constexpr int OFF_Q = 0;                          // two row tiles
-    static constexpr int OFF_KV = OFF_Q + 2 * STAGE;
+    static constexpr int OFF_KV = OFF_Q + 2 * QTILE;
     static constexpr int OFF_BAR = OFF_KV + STAGES * STAGE;
     static constexpr int N_BARS = 2 * STAGES + 8;
     static constexpr int OFF_SLOT = OFF_BAR + N_BARS * 8;
@@ -153,6 +153,35 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
 
 constexpr uint32_t IDESC_B_MN_MAJOR = 1u << 16;
 
+// Probabilities 2^(sc S - base) of one row's 128 scores at sb as bf16 pairs, and
+// their sum.  MASKED: columns from nv on count as -inf.
+template <bool MASKED>
+__device__ __forceinline__ float prefix_softmax(uint32_t sb, int nv, float sc, float base, uint32_t (&pk)[PA_KEYS / 2]) {
+    float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+    const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
+#pragma unroll
+    for (int c = 0; c < PA_KEYS / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(sb + c * 32, v);
+        tmem_ld_wait(v);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            float2 s = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            if (MASKED) {
+                if (c * 32 + e >= nv) s.x = -INFINITY;
+                if (c * 32 + e + 1 >= nv) s.y = -INFINITY;
+            }
+            const float2 x = __ffma2_rn(s, sc2, nb2);
+            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            acc[(e >> 1) & 1] = __fadd2_rn(acc[(e >> 1) & 1], p);
+            __nv_bfloat162 pp = __floats2bfloat162_rn(p.x, p.y);
+            pk[c * 16 + (e >> 1)] = *reinterpret_cast<uint32_t*>(&pp);
+        }
+    }
+    const float2 s2 = __fadd2_rn(acc[0], acc[1]);
+    return s2.x + s2.y;
+}
+
 // tmap_kp, tmap_vp: {D, Hkv, P}, box {64, 1, 128}; tmap_k, tmap_v: {D, Hkv, S,
 // B}, box {64, 1, 128, 1}; keys past the end read as zeros.
 template <int D>
@@ -162,10 +191,11 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                    const PrefixAttnArgs a) {
     using S = PrefixSmem<D>;
     constexpr int NST = S::STAGES;
-    constexpr int BOX = PA_TILE * 128;                       // bytes of one 64-column box
+    constexpr int QBOX = PA_ROWS * 128, BOX = PA_KEYS * 128;  // bytes of one 64-column box
+    static_assert(QBOX == BOX, "one offset for both operands of S");
     constexpr uint32_t O_COL = 256;
     extern __shared__ uint8_t pa_raw[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
     // ---------------- the unit: rows r0 .. of one K/V head, keys [key0, key_end)
     int u = blockIdx.x;
@@ -178,9 +208,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         j = u / a.p_splits;
         bi0 = 0;
         n_rows = a.B * a.Lq * a.G;
-        r0 = ru * (a.shared ? 2 * PA_TILE : PA_TILE);
-        key0 = sp * a.p_tps * PA_TILE;
-        key_end = (int)min((long long)a.P, (long long)key0 + (long long)a.p_tps * PA_TILE);
+        r0 = ru * (a.shared ? 2 * PA_ROWS : PA_ROWS);
+        key0 = sp * a.p_tps * PA_KEYS;
+        key_end = (int)min((long long)a.P, (long long)key0 + (long long)a.p_tps * PA_KEYS);
         slot = a.p_streams * sp;
     } else {
         u -= a.n_prefix;
@@ -192,23 +222,23 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         b = u / a.Hkv;
         bi0 = b * a.Lq;
         n_rows = a.Lq * a.G;
-        r0 = ru * PA_TILE;
-        own_len = seq_len(a.lens, b, a.S);
-        const int i_last = (min(r0 + PA_TILE, n_rows) - 1) / a.G;
+        r0 = ru * PA_ROWS;
+        own_len = warp_uniform(seq_len(a.lens, b, a.S));
+        const int i_last = (min(r0 + PA_ROWS, n_rows) - 1) / a.G;
         const int vis = max(0, own_len - a.Lq + i_last + 1);           // of the last row: the most
-        key0 = sp * a.o_tps * PA_TILE;
-        key_end = (int)min((long long)vis, (long long)key0 + (long long)a.o_tps * PA_TILE);
+        key0 = sp * a.o_tps * PA_KEYS;
+        key_end = (int)min((long long)vis, (long long)key0 + (long long)a.o_tps * PA_KEYS);
         slot = a.o_slot0 + a.o_streams * sp;
     }
     const bool shared = prefix && a.shared;
-    const int nt = key_end > key0 ? (key_end - key0 + PA_TILE - 1) / PA_TILE : 0;
+    const int nt = key_end > key0 ? (key_end - key0 + PA_KEYS - 1) / PA_KEYS : 0;
     const int steps = shared ? 2 * nt : nt;
 
     // ---------------- softmax threads: their row
     const int stream = warp >= 8 ? 1 : 0;
     const int wq = warp & 3;                                           // TMEM lane quarter
     const int tr = wq * 32 + lane;                                     // row of the tile
-    const int r = r0 + (shared ? stream * PA_TILE : 0) + tr;
+    const int r = r0 + (shared ? stream * PA_ROWS : 0) + tr;
     const bool row_ok = warp >= 4 && r < n_rows;
     const int bi = bi0 + r / a.G;                                      // b * Lq + i
     const long long row = (long long)bi * a.Hq + j * a.G + r % a.G;
@@ -236,9 +266,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
     uint64_t* full = bars;                       // [NST]
     uint64_t* empty = bars + NST;                // [NST]
     uint64_t* q_full = bars + 2 * NST;
-    uint64_t* s_full = bars + 2 * NST + 1;       // [2]
-    uint64_t* p_full = bars + 2 * NST + 3;       // [2]
-    uint64_t* o_full = bars + 2 * NST + 5;       // [2]
+    uint64_t* s_full = bars + 2 * NST + 1;       // [stream]
+    uint64_t* p_full = bars + 2 * NST + 3;       // [stream]
+    uint64_t* o_full = bars + 2 * NST + 5;       // [stream]
     uint64_t* mma_done = bars + 2 * NST + 7;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_SLOT);
     if (threadIdx.x == 0) {
@@ -262,10 +292,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = warp_uniform(*tmem_slot);
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PA_REGS_CONTROL));
         if (warp == 0 && lane == 0) {
             const CUtensorMap* mk = prefix ? &tmap_kp : &tmap_k;
             const CUtensorMap* mv = prefix ? &tmap_vp : &tmap_v;
@@ -278,7 +307,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                 if (it >= NST && !mbar_wait(&empty[st], ((it / NST) & 1) ^ 1)) break;
                 uint8_t* dst = smem + S::OFF_KV + st * S::STAGE;
                 const CUtensorMap* m = (it & 1) ? mv : mk;
-                const int key = key0 + (it >> 1) * PA_TILE;
+                const int key = key0 + (it >> 1) * PA_KEYS;
                 mbar_arrive_expect_tx(&full[st], (uint32_t)S::STAGE);
                 for (int kb = 0; kb < D / 64; ++kb) {
                     if (prefix) tma_load_3d(dst + kb * BOX, m, &full[st], kb * 64, j, key);
@@ -288,113 +317,107 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             // never leave with copies in flight
             for (int c = max(0, it - NST); c < it; ++c) mbar_wait(&full[c % NST], (c / NST) & 1);
         }
-        if (warp == 1 && lane == 0) {
-            constexpr uint32_t idesc_s = idesc_bf16_f32(128, PA_TILE);
-            constexpr uint32_t idesc_o = idesc_bf16_f32(128, D) | IDESC_B_MN_MAJOR;
+        if (warp == 1) {
+            // the whole warp walks the loop, so that addresses stay in uniform
+            // registers; one elected lane issues (a lane-0 branch spent 1.5 us of
+            // a 2 us step moving descriptors into place)
+            constexpr uint32_t idesc_s = idesc_bf16_f32(PA_ROWS, PA_KEYS);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(PA_ROWS, D) | IDESC_B_MN_MAJOR;
             const uint32_t q_lo = sw128_desc_lo(smem_u32(smem + S::OFF_Q), 16);
-            const uint32_t kv_addr = smem_u32(smem + S::OFF_KV);
-            bool ok = mbar_wait(q_full, 0);
+            const uint32_t k_lo = sw128_desc_lo(smem_u32(smem + S::OFF_KV), 16);
+            const uint32_t v_lo = sw128_desc_lo(smem_u32(smem + S::OFF_KV), BOX);
+            auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
+            bool ok = wait(q_full, 0);
             for (int n = 0; n <= steps && ok; ++n) {
                 if (n < steps) {
                     const int s = n & 1, t = shared ? n >> 1 : n, item = 2 * t, st = item % NST;
-                    if (!(ok = mbar_wait(&full[st], (item / NST) & 1))) break;
-                    if (n >= 2 && !(ok = mbar_wait(&o_full[s], ((n >> 1) - 1) & 1))) break;
+                    if (!(ok = wait(&full[st], (item / NST) & 1))) break;
+                    if (n >= 2 && !(ok = wait(&o_full[s], ((n >> 1) & 1) ^ 1))) break;
                     tc_fence_after();
-                    const uint32_t qa = q_lo + (uint32_t)(shared ? s * (S::STAGE >> 4) : 0);
-                    const uint32_t ka = sw128_desc_lo(kv_addr + st * S::STAGE, 16);
+                    const uint32_t qa = q_lo + (uint32_t)(shared ? s * (S::QTILE >> 4) : 0);
+                    const uint32_t ka = k_lo + (uint32_t)(st * (S::STAGE >> 4));
+                    const uint32_t dst = tmem + (uint32_t)(s * PA_KEYS);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t o = (uint32_t)((kk >> 2) * BOX + (kk & 3) * 32) >> 4;
-                        tc_mma_ss(tmem + (uint32_t)(s * PA_TILE), qa + o, ka + o, idesc_s, kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t o = (uint32_t)((kk >> 2) * BOX + (kk & 3) * 32) / 16;
+                            tc_mma_ss(dst, qa + o, ka + o, idesc_s, kk > 0 ? 1u : 0u);
+                        }
+                        tc_commit(&s_full[s]);
+                        if (!shared || s == 1) tc_commit(&empty[st]);
                     }
-                    tc_commit(&s_full[s]);
-                    if (!shared || s == 1) tc_commit(&empty[st]);
                 }
                 if (n > 0) {
                     const int m = n - 1, s = m & 1, t = shared ? m >> 1 : m, item = 2 * t + 1, st = item % NST;
-                    if (!(ok = mbar_wait(&full[st], (item / NST) & 1))) break;
-                    if (!(ok = mbar_wait(&p_full[s], (m >> 1) & 1))) break;
+                    if (!(ok = wait(&full[st], (item / NST) & 1))) break;
+                    if (!(ok = wait(&p_full[s], (m >> 1) & 1))) break;
                     tc_fence_after();
-                    const uint32_t va = sw128_desc_lo(kv_addr + st * S::STAGE, BOX);
+                    const uint32_t va = v_lo + (uint32_t)(st * (S::STAGE >> 4));
+                    const uint32_t dst = tmem + O_COL + (uint32_t)(s * D), src = tmem + (uint32_t)(s * PA_KEYS);
+                    if (elect_one()) {
+                        tc_mma_ts(dst, src, va, idesc_o, m >= 2 ? 1u : 0u);
 #pragma unroll
-                    for (int kk = 0; kk < PA_TILE / 16; ++kk)
-                        tc_mma_ts(tmem + O_COL + (uint32_t)(s * D), tmem + (uint32_t)(s * PA_TILE + kk * 8),
-                                  va + (uint32_t)(kk * 2048 >> 4), idesc_o, (m >= 2 || kk > 0) ? 1u : 0u);
-                    tc_commit(&o_full[s]);
-                    if (!shared || s == 1) tc_commit(&empty[st]);
+                        for (int kk = 1; kk < PA_KEYS / 16; ++kk)
+                            tc_mma_ts(dst, src + (uint32_t)(kk * 8), va + (uint32_t)(kk * 2048 >> 4), idesc_o, 1u);
+                        tc_commit(&o_full[s]);
+                        if (!shared || s == 1) tc_commit(&empty[st]);
+                    }
                 }
             }
-            // the MMAs this thread issued are done before TMEM is freed
-            tc_commit(mma_done);
+            // the MMAs this warp issued are done before TMEM is freed
+            if (elect_one()) tc_commit(mma_done);
+            __syncwarp();
             mbar_wait(mma_done, 0);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PA_REGS_SOFTMAX));
-        // the row's query to shared memory (rows past the last are zero);
-        // split units have one tile, which the first warpgroup writes
+        // the rows' queries to shared memory, a warp its own 32 rows, 16 bytes
+        // a lane (rows past the last are zero); split units have one row tile,
+        // which the first warpgroup writes
+        const long long my_row = row_ok ? row : -1;
         if (shared || stream == 0) {
-            const uint4* src = reinterpret_cast<const uint4*>(a.q + row * D);
-            uint8_t* dst = smem + S::OFF_Q + (shared ? stream * S::STAGE : 0) + tr * 128;
-            uint4 v[D / 8];
+            constexpr int LPR = D / 8, RPI = 32 / LPR;                 // lanes a row, rows an access
+            uint8_t* dst = smem + S::OFF_Q + (shared ? stream * S::QTILE : 0);
+            const int c = lane % LPR;
+            uint4 v[32 / RPI];
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) v[c] = row_ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+            for (int x = 0; x < 32 / RPI; ++x) {
+                const long long rr = __shfl_sync(0xffffffffu, my_row, x * RPI + lane / LPR);
+                v[x] = rr >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.q + rr * D) + c) : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4*>(dst + (c >> 3) * BOX + (((c & 7) ^ (tr & 7)) << 4)) = v[c];
+            for (int x = 0; x < 32 / RPI; ++x) {
+                const int lr = wq * 32 + x * RPI + lane / LPR;
+                *reinterpret_cast<uint4*>(dst + (c >> 3) * QBOX + lr * 128 + (((c & 7) ^ (lr & 7)) << 4)) = v[x];
+            }
             fence_proxy_async_smem();
         }
         mbar_arrive(q_full);
 
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
-        const uint32_t sb = tmem + lane_base + (uint32_t)(stream * PA_TILE);
+        const uint32_t sb = tmem + lane_base + (uint32_t)(stream * PA_KEYS);
         const uint32_t ob = tmem + lane_base + O_COL + (uint32_t)(stream * D);
         const float sc = a.scale_log2;
         float m_used = -INFINITY, l_run = 0.0f;
         bool ok = true;
         for (int i = 0; i < my_steps; ++i) {
             const int t = shared ? i : 2 * i + stream;
-            const int key = key0 + t * PA_TILE;
+            const int key = key0 + t * PA_KEYS;
             const int nv = min(vis, key_end) - key;                    // columns of the tile this row sees
-            const bool masked = __any_sync(0xffffffffu, nv < PA_TILE);
+            const bool masked = __any_sync(0xffffffffu, nv < PA_KEYS);
             // waits are warp-uniform: the TMEM accesses below are warp-collective
             if (!__all_sync(0xffffffffu, mbar_wait(&s_full[stream], i & 1))) { ok = false; break; }
             tc_fence_after();
-            uint32_t pk[PA_TILE / 2];
+            uint32_t pk[PA_KEYS / 2];
             float rs = 0.0f;
-            // probabilities of the tile (bf16 pairs) against `base`, and their sum
             auto softmax_tile = [&](float base) {
-                float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
-                const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
-                uint32_t v[2][32];
-                tmem_ld_32x32b_x32(sb, v[0]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld_wait(v[c & 1]);
-                    if (c < 3) tmem_ld_32x32b_x32(sb + (c + 1) * 32, v[(c + 1) & 1]);
-                    if (masked) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (c * 32 + e >= nv) v[c & 1][e] = 0xff800000u;      // -inf
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[c & 1][e]),
-                                                                __uint_as_float(v[c & 1][e + 1])), sc2, nb2);
-                        const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                        acc[(e >> 1) & 1] = __fadd2_rn(acc[(e >> 1) & 1], p);
-                        __nv_bfloat162 pp = __floats2bfloat162_rn(p.x, p.y);
-                        pk[c * 16 + (e >> 1)] = *reinterpret_cast<uint32_t*>(&pp);
-                    }
-                }
-                const float2 s2 = __fadd2_rn(acc[0], acc[1]);
-                rs = s2.x + s2.y;
+                rs = masked ? prefix_softmax<true>(sb, nv, sc, base, pk) : prefix_softmax<false>(sb, nv, sc, base, pk);
             };
             // Every branch around TMEM accesses is warp-uniform.  Rows that see
             // nothing of the tile need no maximum (their probabilities are 0).
             const bool fresh = m_used == -INFINITY;
             if (!__any_sync(0xffffffffu, nv > 0)) {
 #pragma unroll
-                for (int e = 0; e < PA_TILE / 2; ++e) pk[e] = 0u;
+                for (int e = 0; e < PA_KEYS / 2; ++e) pk[e] = 0u;
             } else if (!__all_sync(0xffffffffu, fresh && nv > 0)) {
                 softmax_tile(fresh ? 0.0f : m_used);
             }
@@ -403,7 +426,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                 // the tile's maximum; rows that need it move their base to it
                 float mx = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < PA_KEYS / 32; ++c) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(sb + c * 32, v);
                     tmem_ld_wait(v);
@@ -433,7 +456,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             tmem_st_32x32b_x32(sb, *reinterpret_cast<uint32_t (*)[32]>(&pk[0]));
             tmem_st_32x32b_x32(sb + 32, *reinterpret_cast<uint32_t (*)[32]>(&pk[32]));
             tmem_st_wait();
-            if (!prefix && key + PA_TILE > own_len) {
+            if (!prefix && key + PA_KEYS > own_len) {
                 // rows of V past the sequence's length may hold anything: zero
                 // them, since 0 * NaN would reach every output
                 const int item = 2 * t + 1, st = item % NST;
@@ -462,34 +485,42 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                 else if (a.lse) a.lse[row] = lse2 * LN2;
             }
             if (my_steps > 0) {
+                // O / l through shared memory, 32 columns of the warp's 32 rows at
+                // a time, so that global writes are whole 128-byte lines.  The
+                // query tiles are free: every S was issued before the P V that
+                // o_full waited for.
+                uint8_t* stage = smem + S::OFF_Q + (warp - 4) * 4096;
+                const long long dst_row = writes ? (a.slots > 1 ? row * a.slots + my_slot : row) : -1;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     __syncwarp();
                     tmem_ld_32x32b_x32(ob + c * 32, o);
                     tmem_ld_wait(o);
-                    if (!writes) continue;
-                    // a row that saw nothing has P = 0: its O is 0 or, from
-                    // non-finite V, NaN; it is written as 0
-                    float f[32];
+                    // a row that saw nothing has P = 0 and is written as 0
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = l_run == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
-                    if (a.slots > 1) {
-                        float4* dst = reinterpret_cast<float4*>(a.part_o + (row * a.slots + my_slot) * D + c * 32);
+                    for (int e = 0; e < 8; ++e) {
+                        float4 f;
+                        f.x = l_run == 0.0f ? 0.0f : __uint_as_float(o[4 * e]) * inv;
+                        f.y = l_run == 0.0f ? 0.0f : __uint_as_float(o[4 * e + 1]) * inv;
+                        f.z = l_run == 0.0f ? 0.0f : __uint_as_float(o[4 * e + 2]) * inv;
+                        f.w = l_run == 0.0f ? 0.0f : __uint_as_float(o[4 * e + 3]) * inv;
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = f;
+                    }
+                    __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + c * 32);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                __nv_bfloat162 pp = __floats2bfloat162_rn(f[8 * e + 2 * x], f[8 * e + 2 * x + 1]);
-                                w[x] = *reinterpret_cast<uint32_t*>(&pp);
+                    for (int x = 0; x < 8; ++x) {
+                        const int lr = x * 4 + (lane >> 3);
+                        const long long dr = __shfl_sync(0xffffffffu, dst_row, lr);
+                        const float4 f = *reinterpret_cast<const float4*>(stage + lr * 128 + (((lane & 7) ^ (lr & 7)) << 4));
+                        if (dr >= 0) {
+                            if (a.slots > 1) {
+                                reinterpret_cast<float4*>(a.part_o + dr * D + c * 32)[lane & 7] = f;
+                            } else {
+                                __nv_bfloat162 p0 = __floats2bfloat162_rn(f.x, f.y), p1 = __floats2bfloat162_rn(f.z, f.w);
+                                reinterpret_cast<uint2*>(a.out + dr * D + c * 32)[lane & 7] =
+                                    make_uint2(*reinterpret_cast<uint32_t*>(&p0), *reinterpret_cast<uint32_t*>(&p1));
                             }
-                            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
                 }
