@@ -24,11 +24,13 @@
 // Step n of a unit belongs to stream n & 1 and the 128-key tile n >> 1 (shared)
 // or n (split).
 //   warp 0      TMA: 128-key tiles of K and V, alternately, into one ring.
-//   warp 1      TMEM allocation and MMA issue: S(n) = Q K^T (M=128, N=128),
-//               then O += P(n-1) V.  P comes from TMEM, V from its [keys, d]
-//               tile as an MN-major operand (no transposed copy).  S(n)
+//   warp 1      TMEM allocation; issues S(n) = Q K^T (M=128, N=128).  S(n)
 //               overwrites the columns of P(n-2), so it is issued when P(n-2) V
 //               has completed.
+//   warp 2      issues O += P(n) V.  P comes from TMEM, V from its [keys, d]
+//               tile as an MN-major operand (no transposed copy).  A warp of its
+//               own, so that neither kind of MMA waits behind the other's
+//               barriers.
 //   warps 4-7, 8-11  the softmax of stream 0 / 1: thread = row = TMEM lane.
 //               The probabilities against the running maximum are packed to
 //               bf16 and stored over the scores.  Their rounding (2^-8 of each)
@@ -47,6 +49,10 @@
 namespace ic {
 
 constexpr int PA_THREADS = 384;                   // a control warpgroup and one per stream
+// Registers a thread: launched with 168 (65536 / 384, rounded down to 8); the
+// control warpgroup gives some up for the softmax ones.
+constexpr int PA_REGS_CONTROL = 80, PA_REGS_SOFTMAX = 208;
+static_assert(PA_REGS_CONTROL + 2 * PA_REGS_SOFTMAX <= 3 * 168, "register split of the launch");
 constexpr int PA_ROWS = 128;                      // rows per stream
 constexpr int PA_KEYS = 128;                      // keys per tile
 constexpr float PA_SUM_MAX = 4294967296.0f;       // 2^32
@@ -88,7 +94,7 @@ struct PrefixSmem {
     static constexpr int OFF_Q = 0;                          // two row tiles
     static constexpr int OFF_KV = OFF_Q + 2 * QTILE;
     static constexpr int OFF_BAR = OFF_KV + STAGES * STAGE;
-    static constexpr int N_BARS = 2 * STAGES + 8;
+    static constexpr int N_BARS = 2 * STAGES + 10;
     static constexpr int OFF_SLOT = OFF_BAR + N_BARS * 8;
     static constexpr int BYTES = OFF_SLOT + 16;
     static constexpr int ALLOC = BYTES + 1024;               // slack for the 1024-byte alignment
@@ -182,6 +188,23 @@ __device__ __forceinline__ float prefix_softmax(uint32_t sb, int nv, float sc, f
     return s2.x + s2.y;
 }
 
+// The largest of one row's first nv scores among `chunks` x 32 columns at sb
+// (NaN ignored).  Rolled: code that runs once per unit costs its instruction
+// fetches.
+__device__ __forceinline__ float prefix_max(uint32_t sb, int chunks, int nv) {
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(sb + c * 32, v);
+        tmem_ld_wait(v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (c * 32 + e < nv) mx = fmaxf(mx, __uint_as_float(v[e]));
+    }
+    return mx;
+}
+
 // tmap_kp, tmap_vp: {D, Hkv, P}, box {64, 1, 128}; tmap_k, tmap_v: {D, Hkv, S,
 // B}, box {64, 1, 128, 1}; keys past the end read as zeros.
 template <int D>
@@ -270,6 +293,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
     uint64_t* p_full = bars + 2 * NST + 3;       // [stream]
     uint64_t* o_full = bars + 2 * NST + 5;       // [stream]
     uint64_t* mma_done = bars + 2 * NST + 7;
+    uint64_t* turn = bars + 2 * NST + 8;         // [stream]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_SLOT);
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
@@ -277,11 +301,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             mbar_init(&empty[i], 1);
         }
         mbar_init(q_full, 256);
-        mbar_init(mma_done, 1);
+        mbar_init(mma_done, 2);                                        // both issuing warps
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 128);
             mbar_init(&o_full[i], 1);
+            mbar_init(&turn[i], 4);
         }
         fence_barrier_init();
     }
@@ -295,6 +320,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
     const uint32_t tmem = warp_uniform(*tmem_slot);
 
     if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PA_REGS_CONTROL));
         if (warp == 0 && lane == 0) {
             const CUtensorMap* mk = prefix ? &tmap_kp : &tmap_k;
             const CUtensorMap* mv = prefix ? &tmap_vp : &tmap_v;
@@ -317,22 +343,21 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             // never leave with copies in flight
             for (int c = max(0, it - NST); c < it; ++c) mbar_wait(&full[c % NST], (c / NST) & 1);
         }
-        if (warp == 1) {
+        if (warp == 1 || warp == 2) {
             // the whole warp walks the loop, so that addresses stay in uniform
             // registers; one elected lane issues (a lane-0 branch spent 1.5 us of
             // a 2 us step moving descriptors into place)
-            constexpr uint32_t idesc_s = idesc_bf16_f32(PA_ROWS, PA_KEYS);
-            constexpr uint32_t idesc_o = idesc_bf16_f32(PA_ROWS, D) | IDESC_B_MN_MAJOR;
-            const uint32_t q_lo = sw128_desc_lo(smem_u32(smem + S::OFF_Q), 16);
-            const uint32_t k_lo = sw128_desc_lo(smem_u32(smem + S::OFF_KV), 16);
-            const uint32_t v_lo = sw128_desc_lo(smem_u32(smem + S::OFF_KV), BOX);
             auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
-            bool ok = wait(q_full, 0);
-            for (int n = 0; n <= steps && ok; ++n) {
-                if (n < steps) {
+            if (warp == 1) {
+                constexpr uint32_t idesc_s = idesc_bf16_f32(PA_ROWS, PA_KEYS);
+                const uint32_t q_lo = sw128_desc_lo(smem_u32(smem + S::OFF_Q), 16);
+                const uint32_t k_lo = sw128_desc_lo(smem_u32(smem + S::OFF_KV), 16);
+                bool ok = wait(q_full, 0);
+                for (int n = 0; n < steps && ok; ++n) {
                     const int s = n & 1, t = shared ? n >> 1 : n, item = 2 * t, st = item % NST;
-                    if (!(ok = wait(&full[st], (item / NST) & 1))) break;
-                    if (n >= 2 && !(ok = wait(&o_full[s], ((n >> 1) & 1) ^ 1))) break;
+                    if (!shared || s == 0) ok = wait(&full[st], (item / NST) & 1);
+                    if (ok && n >= 2) ok = wait(&o_full[s], ((n >> 1) & 1) ^ 1);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t qa = q_lo + (uint32_t)(shared ? s * (S::QTILE >> 4) : 0);
                     const uint32_t ka = k_lo + (uint32_t)(st * (S::STAGE >> 4));
@@ -346,11 +371,17 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                         tc_commit(&s_full[s]);
                         if (!shared || s == 1) tc_commit(&empty[st]);
                     }
+                    __syncwarp();
                 }
-                if (n > 0) {
-                    const int m = n - 1, s = m & 1, t = shared ? m >> 1 : m, item = 2 * t + 1, st = item % NST;
-                    if (!(ok = wait(&full[st], (item / NST) & 1))) break;
-                    if (!(ok = wait(&p_full[s], (m >> 1) & 1))) break;
+            } else {
+                constexpr uint32_t idesc_o = idesc_bf16_f32(PA_ROWS, D) | IDESC_B_MN_MAJOR;
+                const uint32_t v_lo = sw128_desc_lo(smem_u32(smem + S::OFF_KV), BOX);
+                bool ok = true;
+                for (int m = 0; m < steps && ok; ++m) {
+                    const int s = m & 1, t = shared ? m >> 1 : m, item = 2 * t + 1, st = item % NST;
+                    if (!shared || s == 0) ok = wait(&full[st], (item / NST) & 1);
+                    if (ok) ok = wait(&p_full[s], (m >> 1) & 1);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t va = v_lo + (uint32_t)(st * (S::STAGE >> 4));
                     const uint32_t dst = tmem + O_COL + (uint32_t)(s * D), src = tmem + (uint32_t)(s * PA_KEYS);
@@ -362,14 +393,16 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                         tc_commit(&o_full[s]);
                         if (!shared || s == 1) tc_commit(&empty[st]);
                     }
+                    __syncwarp();
                 }
             }
-            // the MMAs this warp issued are done before TMEM is freed
+            // the MMAs these warps issued are done before TMEM is freed
             if (elect_one()) tc_commit(mma_done);
             __syncwarp();
             mbar_wait(mma_done, 0);
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PA_REGS_SOFTMAX));
         // the rows' queries to shared memory, a warp its own 32 rows, 16 bytes
         // a lane (rows past the last are zero); split units have one row tile,
         // which the first warpgroup writes
@@ -397,61 +430,62 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         const uint32_t sb = tmem + lane_base + (uint32_t)(stream * PA_KEYS);
         const uint32_t ob = tmem + lane_base + O_COL + (uint32_t)(stream * D);
         const float sc = a.scale_log2;
+        // keys below vis_k are this row's; lanes without a row go along with
+        // the others' (their query is 0)
+        const bool any_row = __any_sync(0xffffffffu, row_ok);
+        const int vis_k = row_ok ? min(vis, key_end) : (any_row ? key_end : 0);
+        const int vis_least = __reduce_min_sync(0xffffffffu, vis_k), vis_most = __reduce_max_sync(0xffffffffu, vis_k);
         float m_used = -INFINITY, l_run = 0.0f;
         bool ok = true;
         for (int i = 0; i < my_steps; ++i) {
             const int t = shared ? i : 2 * i + stream;
             const int key = key0 + t * PA_KEYS;
-            const int nv = min(vis, key_end) - key;                    // columns of the tile this row sees
-            const bool masked = __any_sync(0xffffffffu, nv < PA_KEYS);
+            const int nv = vis_k - key;                                // columns of the tile this row sees
+            const bool masked = vis_least < key + PA_KEYS;             // some row of the warp does not see all
             // waits are warp-uniform: the TMEM accesses below are warp-collective
             if (!__all_sync(0xffffffffu, mbar_wait(&s_full[stream], i & 1))) { ok = false; break; }
             tc_fence_after();
+            // shared units: the streams' exponentials take turns, so that one
+            // stream's MMAs run meanwhile (left alone the streams fall into step)
+            if (shared && (i > 0 || stream == 1) &&
+                !__all_sync(0xffffffffu, mbar_wait(&turn[stream], stream == 0 ? (i & 1) ^ 1 : i & 1))) { ok = false; break; }
             uint32_t pk[PA_KEYS / 2];
             float rs = 0.0f;
-            auto softmax_tile = [&](float base) {
-                rs = masked ? prefix_softmax<true>(sb, nv, sc, base, pk) : prefix_softmax<false>(sb, nv, sc, base, pk);
-            };
-            // Every branch around TMEM accesses is warp-uniform.  Rows that see
-            // nothing of the tile need no maximum (their probabilities are 0).
-            const bool fresh = m_used == -INFINITY;
-            if (!__any_sync(0xffffffffu, nv > 0)) {
+            // Every branch around TMEM accesses is warp-uniform.
+            if (vis_most <= key) {                                     // no row of the warp sees any
 #pragma unroll
                 for (int e = 0; e < PA_KEYS / 2; ++e) pk[e] = 0u;
-            } else if (!__all_sync(0xffffffffu, fresh && nv > 0)) {
-                softmax_tile(fresh ? 0.0f : m_used);
-            }
-            const bool need_max = nv > 0 && (fresh || !(rs <= PA_SUM_MAX));
-            if (__any_sync(0xffffffffu, need_max)) {
-                // the tile's maximum; rows that need it move their base to it
-                float mx = -INFINITY;
+            } else {
+                // A first base: the maximum of the first 32 columns.
+                if (i == 0) m_used = prefix_max(sb, 1, nv) * sc;
+                for (int attempt = 0;; ++attempt) {
+                    const float base = m_used == -INFINITY ? 0.0f : m_used;
+                    rs = masked ? prefix_softmax<true>(sb, nv, sc, base, pk) : prefix_softmax<false>(sb, nv, sc, base, pk);
+                    // rows that see something and have no base yet, or whose sum
+                    // is too large (or not a number), take the tile's maximum
+                    const bool need_max = nv > 0 && (m_used == -INFINITY || !(rs <= PA_SUM_MAX));
+                    if (attempt > 0 || !__any_sync(0xffffffffu, need_max)) break;
+                    const float mx = prefix_max(sb, PA_KEYS / 32, nv);
+                    const float m_new = need_max ? fmaxf(m_used, mx * sc) : m_used;
+                    const float alpha = m_new == m_used ? 1.0f : ex2_approx(m_used - m_new);   // 0 on a first raise
+                    if (i > 0) {
+                        // S(i) was issued after P(i-1) V(i-1) completed: O is at rest
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(ob + c * 32, o);
+                            tmem_ld_wait(o);
 #pragma unroll
-                for (int c = 0; c < PA_KEYS / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(sb + c * 32, v);
-                    tmem_ld_wait(v);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c * 32 + e < nv) mx = fmaxf(mx, __uint_as_float(v[e]));
-                }
-                const float m_new = need_max ? fmaxf(m_used, mx * sc) : m_used;
-                const float alpha = m_new == m_used ? 1.0f : ex2_approx(m_used - m_new);   // 0 on a first raise
-                if (i > 0) {
-                    // S(i) was issued after P(i-1) V(i-1) completed: O is at rest
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(ob + c * 32, o);
-                        tmem_ld_wait(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st_32x32b_x32(ob + c * 32, o);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st_32x32b_x32(ob + c * 32, o);
+                        }
                     }
+                    l_run *= alpha;
+                    m_used = m_new;
                 }
-                l_run *= alpha;
-                m_used = m_new;
-                softmax_tile(m_new == -INFINITY ? 0.0f : m_new);
             }
+            __syncwarp();
+            if (shared && lane == 0) mbar_arrive(&turn[stream ^ 1]);
             l_run += rs;
             tmem_st_32x32b_x32(sb, *reinterpret_cast<uint32_t (*)[32]>(&pk[0]));
             tmem_st_32x32b_x32(sb + 32, *reinterpret_cast<uint32_t (*)[32]>(&pk[32]));
@@ -491,7 +525,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                 // o_full waited for.
                 uint8_t* stage = smem + S::OFF_Q + (warp - 4) * 4096;
                 const long long dst_row = writes ? (a.slots > 1 ? row * a.slots + my_slot : row) : -1;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     __syncwarp();
@@ -499,16 +533,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                     tmem_ld_wait(o);
                     // a row that saw nothing has P = 0 and is written as 0
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float4 f;
-                        f.x = l_run == 0.0f ? 0.0f : __uint_as_float(o[4 * e]) * inv;
-                        f.y = l_run == 0.0f ? 0.0f : __uint_as_float(o[4 * e + 1]) * inv;
-                        f.z = l_run == 0.0f ? 0.0f : __uint_as_float(o[4 * e + 2]) * inv;
-                        f.w = l_run == 0.0f ? 0.0f : __uint_as_float(o[4 * e + 3]) * inv;
-                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = f;
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                            make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                        __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
                     __syncwarp();
-#pragma unroll
+#pragma unroll 2
                     for (int x = 0; x < 8; ++x) {
                         const int lr = x * 4 + (lane >> 3);
                         const long long dr = __shfl_sync(0xffffffffu, dst_row, lr);
