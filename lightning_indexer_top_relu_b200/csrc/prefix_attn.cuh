@@ -295,6 +295,18 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
     uint64_t* mma_done = bars + 2 * NST + 7;
     uint64_t* turn = bars + 2 * NST + 8;         // [stream]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_SLOT);
+    const CUtensorMap* mk = prefix ? &tmap_kp : &tmap_k;
+    const CUtensorMap* mv = prefix ? &tmap_vp : &tmap_v;
+    auto load_item = [&](int it) {                                     // K (even) or V of a tile into its stage
+        const int st = it % NST, key = key0 + (it >> 1) * PA_KEYS;
+        uint8_t* dst = smem + S::OFF_KV + st * S::STAGE;
+        const CUtensorMap* m = (it & 1) ? mv : mk;
+        mbar_arrive_expect_tx(&full[st], (uint32_t)S::STAGE);
+        for (int kb = 0; kb < D / 64; ++kb) {
+            if (prefix) tma_load_3d(dst + kb * BOX, m, &full[st], kb * 64, j, key);
+            else tma_load_4d(dst + kb * BOX, m, &full[st], kb * 64, j, key, b);
+        }
+    };
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 1);
@@ -309,6 +321,23 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             mbar_init(&turn[i], 4);
         }
         fence_barrier_init();
+        // the first tiles are on their way before anything else is set up
+        tma_prefetch_desc(mk);
+        tma_prefetch_desc(mv);
+        for (int it = 0; it < min(2 * nt, NST); ++it) load_item(it);
+    }
+    // the rows' queries, a warp its own 32 rows, 16 bytes a lane (rows past the
+    // last are zero); split units have one row tile, which the first warpgroup loads
+    constexpr int LPR = D / 8, RPI = 32 / LPR;                         // lanes a row, rows an access
+    const bool loads_q = warp >= 4 && (shared || stream == 0);
+    uint4 qv[32 / RPI];
+    if (loads_q) {
+        const long long my_row = row_ok ? row : -1;
+#pragma unroll
+        for (int x = 0; x < 32 / RPI; ++x) {
+            const long long rr = __shfl_sync(0xffffffffu, my_row, x * RPI + lane / LPR);
+            qv[x] = rr >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.q + rr * D) + lane % LPR) : make_uint4(0, 0, 0, 0);
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
@@ -322,23 +351,11 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PA_REGS_CONTROL));
         if (warp == 0 && lane == 0) {
-            const CUtensorMap* mk = prefix ? &tmap_kp : &tmap_k;
-            const CUtensorMap* mv = prefix ? &tmap_vp : &tmap_v;
-            tma_prefetch_desc(mk);
-            tma_prefetch_desc(mv);
             const int items = 2 * nt;                                  // K(0) V(0) K(1) V(1) ...
-            int it = 0;
+            int it = min(items, NST);
             for (; it < items; ++it) {
-                const int st = it % NST;
-                if (it >= NST && !mbar_wait(&empty[st], ((it / NST) & 1) ^ 1)) break;
-                uint8_t* dst = smem + S::OFF_KV + st * S::STAGE;
-                const CUtensorMap* m = (it & 1) ? mv : mk;
-                const int key = key0 + (it >> 1) * PA_KEYS;
-                mbar_arrive_expect_tx(&full[st], (uint32_t)S::STAGE);
-                for (int kb = 0; kb < D / 64; ++kb) {
-                    if (prefix) tma_load_3d(dst + kb * BOX, m, &full[st], kb * 64, j, key);
-                    else tma_load_4d(dst + kb * BOX, m, &full[st], kb * 64, j, key, b);
-                }
+                if (!mbar_wait(&empty[it % NST], ((it / NST) & 1) ^ 1)) break;
+                load_item(it);
             }
             // never leave with copies in flight
             for (int c = max(0, it - NST); c < it; ++c) mbar_wait(&full[c % NST], (c / NST) & 1);
@@ -403,24 +420,13 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PA_REGS_SOFTMAX));
-        // the rows' queries to shared memory, a warp its own 32 rows, 16 bytes
-        // a lane (rows past the last are zero); split units have one row tile,
-        // which the first warpgroup writes
-        const long long my_row = row_ok ? row : -1;
-        if (shared || stream == 0) {
-            constexpr int LPR = D / 8, RPI = 32 / LPR;                 // lanes a row, rows an access
+        if (loads_q) {
             uint8_t* dst = smem + S::OFF_Q + (shared ? stream * S::QTILE : 0);
             const int c = lane % LPR;
-            uint4 v[32 / RPI];
-#pragma unroll
-            for (int x = 0; x < 32 / RPI; ++x) {
-                const long long rr = __shfl_sync(0xffffffffu, my_row, x * RPI + lane / LPR);
-                v[x] = rr >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.q + rr * D) + c) : make_uint4(0, 0, 0, 0);
-            }
 #pragma unroll
             for (int x = 0; x < 32 / RPI; ++x) {
                 const int lr = wq * 32 + x * RPI + lane / LPR;
-                *reinterpret_cast<uint4*>(dst + (c >> 3) * QBOX + lr * 128 + (((c & 7) ^ (lr & 7)) << 4)) = v[x];
+                *reinterpret_cast<uint4*>(dst + (c >> 3) * QBOX + lr * 128 + (((c & 7) ^ (lr & 7)) << 4)) = qv[x];
             }
             fence_proxy_async_smem();
         }
