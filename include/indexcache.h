@@ -403,12 +403,19 @@ size_t ic_prefix_attn_workspace_bytes(int B, int Lq, int P, int S, int Hq, int H
  * (q_offset + Lq may exceed Lk here: q_offset >= Lk lets every row see every
  * key, as the rows of a batch see a shared prefix).  Rows with
  * lse = -INFINITY add nothing.  Positions that no row sees keep their value,
- * and their keys may hold anything.  Shapes as in ic_prefix_attn.  The sum has a fixed order:
- * the same call gives the same bits.
+ * and their keys may hold anything.  Heads and d as in ic_prefix_attn; B <=
+ * 65535, Lk <= 2^30, Lq <= 2^29.  The sum has a fixed order: the same call gives
+ * the same bits.
+ * ws/ws_bytes: device workspace of ic_attn_mass_workspace_bytes(...) bytes for
+ * the sums of rows that several CTAs share (may be NULL when that is 0); less
+ * returns IC_ERR_WORKSPACE_TOO_SMALL.
  */
 int ic_attn_mass(const uint16_t *q, const uint16_t *k, const float *lse, const int32_t *lens, int B,
                  int Lq, int Lk, int Hq, int Hkv, int d, int q_offset, float scale, float *mass,
-                 ic_stream_t stream);
+                 void *ws, size_t ws_bytes, ic_stream_t stream);
+
+/* Workspace ic_attn_mass needs on the current device (0 for invalid sizes). */
+size_t ic_attn_mass_workspace_bytes(int B, int Lq, int Lk, int Hq, int Hkv, int d);
 
 /*
  * ic_attn_mass over the slots of an index cache: every slot of idx

@@ -21,9 +21,11 @@
 //               column's -lse2 = -lse log2 e (-inf for columns without a row, whose
 //               weight is then 0) and the number of positions it sees, read
 //               from global memory a step ahead.
-// When one sequence has few key tiles and many rows, a cluster of up to 8 CTAs
-// shares a key tile: rank r takes every C-th row tile and rank 0 adds the sums
-// through distributed shared memory, in rank order.
+// When there are few key tiles and many rows, `ranks` CTAs share a key tile:
+// rank r takes every ranks-th row tile and writes its sums to the workspace, and
+// attn_mass_add_kernel adds them in rank order.  (Clusters that add through
+// distributed shared memory measured slower: at most 15 clusters of 8 were
+// resident, 120 CTAs where 296 fit.)
 #pragma once
 
 #include "common.cuh"
@@ -44,17 +46,12 @@ struct AttnMassArgs {
     int B, Lq, Lk, Hq, Hkv, G, q_offset;
     int ipt, n_cols;            // queries per row tile; columns of the MMA (a multiple of 16)
     int row_tiles;              // row tiles of a sequence and K/V head
-    int group;                  // key tiles a CTA (1 when a cluster shares a key tile)
+    int group;                  // key tiles a CTA
+    float* part;                // [ranks, B, Lk] sums when several ranks share a key tile
     int q_stages, k_stages;     // ring depths; one row tile in all: q_stages == 1, loaded once
     int q_half;                 // bytes of a row tile's 64-column half: n_cols rows of 128
     float scale_log2;
 };
-
-// Positions that row i of a sequence of n positions sees: [0, returned value).
-__device__ __forceinline__ int mass_limit(const AttnMassArgs& a, int n, int i) {
-    const long long t1 = (a.lens ? (long long)n - a.Lq : (long long)a.q_offset) + i + 1;
-    return (int)max(0LL, min(t1, (long long)n));
-}
 
 template <int D>
 struct MassSmem {
@@ -146,31 +143,30 @@ __device__ __forceinline__ float mass_tile_sum(uint32_t sb, int n_cols, const fl
 }
 
 // tmap_q: {D, G, Hkv, Lq, B}, box {64, G, 1, ipt, 1}; tmap_k: {D, Hkv, Lk, B},
-// box {64, 1, 128, 1}; what lies outside reads as zeros.  Grid: cluster ranks x
-// key groups x B.
+// box {64, 1, 128, 1}; what lies outside reads as zeros.  Grid: ranks x key
+// groups x B.
 template <int D>
 __global__ void __launch_bounds__(AM_THREADS, 2)
 attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                  const AttnMassArgs a) {
     using S = MassSmem<D>;
     extern __shared__ uint8_t am_raw[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int rank = blockIdx.x, C = gridDim.x, b = blockIdx.z;
-    const int n = seq_len(a.lens, b, a.Lk);
+    const int n = warp_uniform(seq_len(a.lens, b, a.Lk));
     const int kt0 = blockIdx.y * a.group;
     const int kt1 = min(kt0 + a.group, (n + AM_TILE - 1) / AM_TILE);
-    // first row that sees key 0 of a tile: t = base + i >= key
-    const long long base = a.lens ? (long long)n - a.Lq : (long long)a.q_offset;
-    auto first_tile = [&](int kt) {
-        return (int)(min((long long)a.Lq, max(0LL, (long long)kt * AM_TILE - base)) / a.ipt);
-    };
+    // row i is at t = base + i (Lk <= 2^30, Lq <= 2^29): it sees [0, limit)
+    const int base = a.lens ? n - a.Lq : min(a.q_offset, 1 << 30);     // from Lk on, every row sees every key
+    auto limit = [&](int i) { return max(0, min(base + i + 1, n)); };
+    // row tiles that see a key tile: first_tile .. row_tiles - 1, as its first key is seen from row key - base on
+    auto first_tile = [&](int kt) { return max(0, kt * AM_TILE - base) / a.ipt; };
     // steps of key tile kt: for each K/V head, row tiles first_tile + rank, + C, ...
     auto rows_of = [&](int kt) {
-        const long long f = min((long long)a.Lq, max(0LL, (long long)kt * AM_TILE - base));
-        const int f0 = (int)(f / a.ipt);
-        return f >= a.Lq || f0 + rank >= a.row_tiles ? 0 : (a.row_tiles - f0 - rank + C - 1) / C;
+        const int f0 = first_tile(kt) + rank;
+        return kt * AM_TILE - base >= a.Lq || f0 >= a.row_tiles ? 0 : (a.row_tiles - f0 + C - 1) / C;
     };
-    if (kt0 >= kt1) return;                                     // uniform over the cluster
+    if (kt0 >= kt1) return;
     const int q_bytes = a.q_half * (D / 64);
     const int stage_bytes = a.q_stages * q_bytes + a.k_stages * S::K_BYTES;
     uint8_t* smem = align_smem_1024(am_raw, (uint32_t)(stage_bytes + S::TAIL));
@@ -214,7 +210,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        const uint32_t tmem = *tmem_slot;
+        const uint32_t tmem = warp_uniform(*tmem_slot);
 
         if (warp == 0) {
             int kn = 0, qn = 0;                                 // K tiles and row tiles loaded so far
@@ -256,39 +252,47 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 for (int c = max(0, qn - 2); c < qn; ++c) mbar_wait(&q_full[c & 1], (c >> 1) & 1);
             }
         } else if (warp == 1) {
-            if (lane == 0) {
-                const uint32_t idesc = idesc_bf16_f32(128, a.n_cols);
-                int kn = 0, step = 0;
-                bool ok = true;
-                for (int kt = kt0; kt < kt1 && ok; ++kt) {
-                    const int nr = rows_of(kt);
-                    for (int j = 0; j < a.Hkv && ok && nr > 0; ++j, ++kn) {
-                        const int ks = kn % a.k_stages;
-                        if (!(ok = mbar_wait(&k_full[ks], (kn / a.k_stages) & 1))) break;
-                        const uint32_t ka = sw128_desc_lo(smem_u32(sk + ks * S::K_BYTES), 16);
-                        for (int x = 0; x < nr; ++x, ++step) {
-                            const int qs = resident ? 0 : step & 1, buf = step & 1;
-                            if (!(ok = mbar_wait(&q_full[qs], resident ? 0 : (step >> 1) & 1))) break;
-                            if (step >= 2 && !(ok = mbar_wait(&s_empty[buf], ((step >> 1) & 1) ^ 1))) break;
-                            tc_fence_after();
-                            const uint32_t qa = sw128_desc_lo(smem_u32(sq + qs * q_bytes), 16);
+            // the whole warp walks the loop, so that addresses stay in uniform
+            // registers; one elected lane issues
+            auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
+            const uint32_t idesc = idesc_bf16_f32(128, a.n_cols);
+            const uint32_t k_lo = sw128_desc_lo(smem_u32(sk), 16), q_lo = sw128_desc_lo(smem_u32(sq), 16);
+            const uint32_t q_half16 = (uint32_t)a.q_half / 16;
+            int kn = 0, ks = 0, step = 0;
+            bool ok = true;
+            for (int kt = kt0; kt < kt1 && ok; ++kt) {
+                const int nr = rows_of(kt);
+                for (int j = 0; j < a.Hkv && nr > 0; ++j, ++kn) {
+                    if (!(ok = wait(&k_full[ks], (kn / a.k_stages) & 1))) break;
+                    const uint32_t ka = k_lo + (uint32_t)(ks * (S::K_BYTES >> 4));
+                    for (int x = 0; x < nr; ++x, ++step) {
+                        const int qs = resident ? 0 : step & 1, buf = step & 1;
+                        if (!resident || step == 0) ok = wait(&q_full[qs], resident ? 0 : (step >> 1) & 1);
+                        if (ok && step >= 2) ok = wait(&s_empty[buf], ((step >> 1) & 1) ^ 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t qa = q_lo + (uint32_t)(qs * q_bytes) / 16;
+                        const uint32_t dst = tmem + (uint32_t)(buf * AM_TILE);
+                        if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t o = (uint32_t)((kk & 3) * 32) >> 4;
-                                tc_mma_ss(tmem + (uint32_t)(buf * AM_TILE),
-                                          ka + o + (uint32_t)((kk >> 2) * AM_TILE * 128 >> 4),
-                                          qa + o + (uint32_t)((kk >> 2) * a.q_half) / 16, idesc, kk > 0 ? 1u : 0u);
-                            }
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                tc_mma_ss(dst, ka + (uint32_t)((kk >> 2) * AM_TILE * 128 + (kk & 3) * 32) / 16,
+                                          qa + (uint32_t)(kk >> 2) * q_half16 + (uint32_t)((kk & 3) * 2), idesc,
+                                          kk > 0 ? 1u : 0u);
                             tc_commit(&s_full[buf]);
                             if (!resident) tc_commit(&q_empty[qs]);
+                            if (x == nr - 1) tc_commit(&k_empty[ks]);
                         }
-                        if (ok) tc_commit(&k_empty[ks]);
+                        __syncwarp();
                     }
+                    if (!ok) break;
+                    ks = ks + 1 == a.k_stages ? 0 : ks + 1;
                 }
-                // the MMAs this thread issued are done before TMEM is freed
-                tc_commit(mma_done);
-                mbar_wait(mma_done, 0);
             }
+            // the MMAs this warp issued are done before TMEM is freed
+            if (elect_one()) tc_commit(mma_done);
+            __syncwarp();
+            mbar_wait(mma_done, 0);
         } else {
             const int g = warp >= 6 ? 1 : 0;                    // warpgroup = buffer
             const int tr = (warp & 3) * 32 + lane;              // key of the tile = TMEM lane
@@ -299,9 +303,9 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             const bool has_col = ii < a.ipt;
             const float* lse_col = a.lse + ((long long)b * a.Lq + ii) * a.Hq + tr % a.G;
             float* cols = reinterpret_cast<float*>(tail + S::COLS + g * 2 * S::COL_STAGE);
-            // lse of this thread's column in step x of a key tile (+inf: no row)
-            auto load_lse = [&](int x, int nr, int f0) {
-                const int j = x / nr, i0 = (f0 + rank + (x - j * nr) * C) * a.ipt;
+            // lse of this thread's column of the row tile from query i0 on and
+            // K/V head j (+inf: no row)
+            auto load_lse = [&](int i0, int j) {
                 return has_col && i0 + ii < a.Lq ? __ldg(lse_col + (long long)i0 * a.Hq + j * a.G) : INFINITY;
             };
             int step0 = 0, stage = 0;
@@ -311,18 +315,34 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 const int key = kt * AM_TILE + tr;
                 float total = 0.0f, comp = 0.0f;                // compensated sum over the row tiles
                 int x = (g ^ step0) & 1;                        // this warpgroup's steps of the tile
-                float l = x < steps && !(resident && stage > 0) ? load_lse(x, nr, f0) : 0.0f;
+                // the step's row tile (its first query) and K/V head, and the next step's
+                const int stride = C * a.ipt;
+                int i0 = (f0 + rank) * a.ipt, j = 0, xr = 0;
+                auto advance = [&](int by) {
+                    xr += by;
+                    i0 += by * stride;
+                    while (xr >= nr) {
+                        xr -= nr;
+                        i0 -= nr * stride;
+                        ++j;
+                    }
+                };
+                float l = 0.0f;
+                if (x < steps) {
+                    if (x > 0) advance(x);
+                    if (!(resident && stage > 0)) l = load_lse(i0, j);
+                }
                 for (; x < steps; x += 2) {
-                    const int step = step0 + x;
-                    const int i0 = (f0 + rank + (x % nr) * C) * a.ipt;      // first query of the row tile
+                    const int step = step0 + x, i_first = i0;
+                    if (x + 2 < steps) advance(2);
                     // column info of the row tile, two buffers in turn (a resident one once)
                     if (!resident || stage == 0) {
                         float* cl = cols + (stage & 1) * (S::COL_STAGE / 4);
                         const bool none = l == -INFINITY;       // a row without keys adds nothing
                         cl[tr] = none ? -INFINITY : -l * LOG2E;
-                        reinterpret_cast<int*>(cl)[AM_TILE + tr] = none || l == INFINITY ? 0 : mass_limit(a, n, i0 + ii);
+                        reinterpret_cast<int*>(cl)[AM_TILE + tr] = none || l == INFINITY ? 0 : limit(i_first + ii);
                         empty_row = named_bar_or(2 + g, 128, none);
-                        if (x + 2 < steps) l = load_lse(x + 2, nr, f0);
+                        if (x + 2 < steps) l = load_lse(i0, j);
                     }
                     const float* cl = cols + (resident ? 0 : (stage & 1) * (S::COL_STAGE / 4));
                     const int* lim = reinterpret_cast<const int*>(cl + AM_TILE);
@@ -331,7 +351,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     if (!ok) continue;
                     tc_fence_after();
                     // limits grow with the query: the first one is the least
-                    const bool masked = empty_row || mass_limit(a, n, i0) < (kt + 1) * AM_TILE;
+                    const bool masked = empty_row || limit(i_first) < (kt + 1) * AM_TILE;
                     const float sum = masked ? mass_tile_sum<true>(sb, n_cols, cl, lim, key, a.scale_log2)
                                              : mass_tile_sum<false>(sb, n_cols, cl, lim, key, a.scale_log2);
                     tc_fence_before();
@@ -343,18 +363,17 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     total = t;
                 }
                 step0 += steps;
-                if (C > 1 || steps > 1) {
+                if (steps > 1) {
                     // both warpgroups hold a share of the tile's keys
                     if (g == 1) red[tr] = total;
                     named_bar(1, 256);
-                    if (g == 0) {
-                        total += red[tr];
-                        if (C > 1) red[tr] = total;
-                        else if (key < n) a.mass[(long long)b * a.Lk + key] += total;
-                    }
+                    if (g == 0) total += red[tr];
                     named_bar(1, 256);
-                } else if (steps == 1 && ((step0 - 1) & 1) == g && key < n) {
-                    a.mass[(long long)b * a.Lk + key] += total;
+                }
+                // the warpgroup that has the sum: the first, or the one of a single step
+                if (key < n && g == (steps == 1 ? (step0 - 1) & 1 : 0)) {
+                    if (C > 1) a.part[((long long)rank * a.B + b) * a.Lk + key] = total;
+                    else a.mass[(long long)b * a.Lk + key] += total;
                 }
             }
         }
@@ -364,17 +383,18 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             tc_fence_after();
             tmem_dealloc(tmem, AM_TMEM_COLS);
         }
-        if (C > 1) {
-            // rank 0 adds the ranks' sums of the one key tile in rank order
-            cluster_sync();
-            const int key = kt0 * AM_TILE + (int)threadIdx.x;
-            if (rank == 0 && threadIdx.x < AM_TILE && key < n) {
-                float total = red[threadIdx.x];
-                for (int r = 1; r < C; ++r) total += ld_dsmem_f32(smem_u32(red + threadIdx.x), (uint32_t)r);
-                a.mass[(long long)b * a.Lk + key] += total;
-            }
-            cluster_sync();               // no CTA leaves while rank 0 may read its shared memory
-        }
+    }
+}
+
+// mass += the ranks' sums, in rank order.
+__global__ void attn_mass_add_kernel(const AttnMassArgs a, int ranks) {
+    const int b = blockIdx.y;
+    const int n = seq_len(a.lens, b, a.Lk);
+    for (long long s = (long long)blockIdx.x * blockDim.x + threadIdx.x; s < n; s += (long long)gridDim.x * blockDim.x) {
+        const long long e = (long long)b * a.Lk + s;
+        float total = 0.0f;
+        for (int r = 0; r < ranks; ++r) total += a.part[(long long)r * a.B * a.Lk + e];
+        a.mass[e] += total;
     }
 }
 

@@ -25,10 +25,18 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// Sizes whose positions the kernels count in 32 bits.
+int check_mass_sizes(int B, int Lq, int Lk) {
+    if (B > 65535 || Lk > (1 << 30) || Lq > (1 << 29))
+        return fail(IC_ERR_UNSUPPORTED, "B=%d Lq=%d Lk=%d (supported: B <= 65535, Lk <= 2^30, Lq <= 2^29)",
+                    B, Lq, Lk);
+    return IC_OK;
+}
+
 // Launch shape of the dense accumulated weights.
 struct MassGeom {
     int G, ipt, n_cols, row_tiles, key_tiles, group, ranks, q_stages, k_stages;
-    size_t smem;
+    size_t smem, ws_bytes;
 };
 
 MassGeom mass_geom(int B, int Lq, int Lk, int Hq, int Hkv, int d, int sms) {
@@ -42,15 +50,14 @@ MassGeom mass_geom(int B, int Lq, int Lk, int Hq, int Hkv, int d, int sms) {
     const long long tiles = (long long)B * g.key_tiles;
     const long long steps = (long long)g.row_tiles * Hkv;          // of a key tile that every row sees
     const long long slots = 2LL * sms;                             // CTAs at once
-    // few key tiles: up to 8 CTAs share one, with at least 4 row tiles each
-    g.ranks = 1;
-    while (g.ranks < 8 && tiles * g.ranks < 2 * slots && g.row_tiles / (2 * g.ranks) >= 4) g.ranks *= 2;
+    // few key tiles: several CTAs share one, with at least 8 steps each, as
+    // long as they fill the GPU four times
+    g.ranks = (int)std::max(1LL, std::min<long long>({32, g.row_tiles / 8, steps / 8, 4 * slots / tiles}));
     // many: CTAs of about 8 steps, as long as they fill the GPU four times
     long long group = g.ranks > 1 ? 1 : std::min((7 + steps) / steps, tiles / (4 * slots));
     group = std::max(group, (g.key_tiles + 65534LL) / 65535);
     g.group = (int)std::max(1LL, std::min<long long>(group, g.key_tiles));
-    if (g.group > 1) g.ranks = 1;
-    if (getenv("AMC")) g.ranks = atoi(getenv("AMC"));
+    g.ws_bytes = g.ranks > 1 ? (size_t)g.ranks * B * Lk * sizeof(float) : 0;
     g.q_stages = steps == 1 ? 1 : 2;
     const int k_bytes = T * d * 2, q_bytes = g.n_cols * d * 2;
     const int tail = d == 64 ? ic::MassSmem<64>::TAIL : ic::MassSmem<128>::TAIL;
@@ -244,9 +251,16 @@ int ic_prefix_attn(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* 
     return launched(cudaGetLastError(), "prefix_attn combine launch");
 }
 
+size_t ic_attn_mass_workspace_bytes(int B, int Lq, int Lk, int Hq, int Hkv, int d) {
+    if (B <= 0 || Lq <= 0 || Lk <= 0 || check_cache_heads(Hq, Hkv, d) || check_mass_sizes(B, Lq, Lk)) return 0;
+    int dev, sms;
+    if (device_setup(&dev, &sms)) sms = 148;
+    return mass_geom(B, Lq, Lk, Hq, Hkv, d, sms).ws_bytes;
+}
+
 int ic_attn_mass(const uint16_t* q, const uint16_t* k, const float* lse, const int32_t* lens, int B,
-                 int Lq, int Lk, int Hq, int Hkv, int d, int q_offset, float scale, float* mass,
-                 ic_stream_t stream) {
+                 int Lq, int Lk, int Hq, int Hkv, int d, int q_offset, float scale, float* mass, void* ws,
+                 size_t ws_bytes, ic_stream_t stream) {
     if (B < 0 || Lq < 0 || Lk < 0 || q_offset < 0)
         return fail(IC_ERR_INVALID_ARG, "negative size (B=%d Lq=%d Lk=%d q_offset=%d)", B, Lq, Lk,
                     q_offset);
@@ -259,12 +273,14 @@ int ic_attn_mass(const uint16_t* q, const uint16_t* k, const float* lse, const i
         return fail(IC_ERR_UNSUPPORTED, "q and k must be 16-byte aligned");
     if (!aligned4(lse) || !aligned4(lens) || !aligned4(mass))
         return fail(IC_ERR_UNSUPPORTED, "lse, lens and mass must be 4-byte aligned");
-    if (B > 65535 || Lk > (1 << 30) || (long long)Lq * Hq > MAX_GRID_X)
-        return fail(IC_ERR_UNSUPPORTED, "B=%d Lq=%d Lk=%d (supported: B <= 65535, Lk <= 2^30, Lq*Hq < 2^31)",
-                    B, Lq, Lk);
+    if (ws_bytes > 0 && !ws) return fail(IC_ERR_INVALID_ARG, "ws is NULL but ws_bytes > 0");
+    if (ws && !aligned16(ws)) return fail(IC_ERR_UNSUPPORTED, "ws must be 16-byte aligned");
+    if ((rc = check_mass_sizes(B, Lq, Lk))) return rc;
     int dev, sms;
     if ((rc = device_setup(&dev, &sms))) return rc;
     const MassGeom g = mass_geom(B, Lq, Lk, Hq, Hkv, d, sms);
+    if (ws_bytes < g.ws_bytes)
+        return fail(IC_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", ws_bytes, g.ws_bytes);
     CUtensorMap tq, tk;
     const uint64_t hd = (uint64_t)Hkv * d, qd = (uint64_t)Hq * d;
     {
@@ -288,21 +304,16 @@ int ic_attn_mass(const uint16_t* q, const uint16_t* k, const float* lse, const i
     a.q_stages = g.q_stages; a.k_stages = g.k_stages; a.q_half = g.n_cols * 128;
     a.scale_log2 = scale_log2_of(scale, d);
     const int groups = (g.key_tiles + g.group - 1) / g.group;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)g.ranks, (unsigned)groups, (unsigned)B);
-    cfg.blockDim = dim3(ic::AM_THREADS);
-    cfg.dynamicSmemBytes = g.smem;
-    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)g.ranks;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    cudaError_t e = d == 64 ? cudaLaunchKernelEx(&cfg, ic::attn_mass_kernel<64>, tq, tk, a)
-                            : cudaLaunchKernelEx(&cfg, ic::attn_mass_kernel<128>, tq, tk, a);
-    return launched(e, "attn_mass launch");
+    a.part = reinterpret_cast<float*>(ws);
+    const dim3 grid((unsigned)g.ranks, (unsigned)groups, (unsigned)B);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (d == 64) ic::attn_mass_kernel<64><<<grid, ic::AM_THREADS, g.smem, st>>>(tq, tk, a);
+    else ic::attn_mass_kernel<128><<<grid, ic::AM_THREADS, g.smem, st>>>(tq, tk, a);
+    if (launched(cudaGetLastError(), "attn_mass launch")) return IC_ERR_CUDA;
+    if (g.ranks == 1) return IC_OK;
+    const dim3 ag((unsigned)std::min(Lk / 256 + 1, 4 * sms), (unsigned)B);
+    ic::attn_mass_add_kernel<<<ag, 256, 0, st>>>(a, g.ranks);
+    return launched(cudaGetLastError(), "attn_mass add launch");
 }
 
 size_t ic_attn_mass_sparse_workspace_bytes(int B, int Lq, int Lk) {

@@ -37,7 +37,8 @@ EXPORTS = ("ic_status_string", "ic_last_error_message", "ic_get_last_device_erro
            "ic_sparse_attn_unique_workspace_bytes", "ic_index_overlap",
            "ic_layer_stack_dense_rows", "ic_layer_stack_forward_opts",
            "ic_layer_stack_fused_fallback_blocks", "ic_prefix_attn",
-           "ic_prefix_attn_workspace_bytes", "ic_attn_mass", "ic_attn_mass_sparse",
+           "ic_prefix_attn_workspace_bytes", "ic_attn_mass",
+           "ic_attn_mass_workspace_bytes", "ic_attn_mass_sparse",
            "ic_attn_mass_sparse_workspace_bytes", "ic_evict_select", "ic_cache_gather")
 
 MARKS_PER_LAYER = 5        # IC_MARKS_PER_LAYER
@@ -134,7 +135,9 @@ _lib.ic_prefix_attn.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, 
 _lib.ic_prefix_attn_workspace_bytes.restype = _Z
 _lib.ic_prefix_attn_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I, _I]
 _lib.ic_attn_mass.restype = _I
-_lib.ic_attn_mass.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P]
+_lib.ic_attn_mass.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _Z, _P]
+_lib.ic_attn_mass_workspace_bytes.restype = _Z
+_lib.ic_attn_mass_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I]
 _lib.ic_attn_mass_sparse.restype = _I
 _lib.ic_attn_mass_sparse.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _Z,
                                      _P]
@@ -419,20 +422,31 @@ def prefix_attn(q, k_prefix, v_prefix, k=None, v=None, lens=None, scale: float =
     return out, lse
 
 
-def attn_mass(q, k, lse, mass, lens=None, q_offset: int = 0, scale: float = 0.0, stream=None):
+def attn_mass_workspace_bytes(B: int, Lq: int, Lk: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(_lib.ic_attn_mass_workspace_bytes(B, Lq, Lk, Hq, Hkv, d))
+
+
+def attn_mass(q, k, lse, mass, lens=None, q_offset: int = 0, scale: float = 0.0, ws=None,
+              stream=None):
     """Adds to mass [B,Lk] fp32 (returned) the attention weight that every
     position of k [B,Lk,Hkv,d] (or [B,Lk,d]) received from the rows of q
     [B,Lq,Hq,d] that see it, summed over rows and heads; lse [B,Lq,Hq] fp32 is
     what the attention call returned.  Row i sees s <= q_offset + i, or with lens
-    [B] int32 s <= lens[b] - Lq + i (ic_attn_mass)."""
+    [B] int32 s <= lens[b] - Lq + i (ic_attn_mass).  ws=None allocates the
+    workspace (attn_mass_workspace_bytes)."""
     B, Lq, Hq, d, Lk, Hkv = _own_shapes(q, k)
     _expect(lse, (B, Lq, Hq), "lse")
     _expect(mass, (B, Lk), "mass")
     _expect(lens, (B,), "lens")
+    if ws is None:
+        nbytes = attn_mass_workspace_bytes(B, Lq, Lk, Hq, Hkv, d)
+        ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8) if nbytes else None
+    nws = 0 if ws is None else ws.numel() * ws.element_size()
     rc = _lib.ic_attn_mass(_ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"),
                            _ptr(lse, torch.float32, "lse"), _ptr(lens, torch.int32, "lens"), B, Lq,
                            Lk, Hq, Hkv, d, q_offset, float(scale),
-                           _ptr(mass, torch.float32, "mass"), _stream(stream))
+                           _ptr(mass, torch.float32, "mass"),
+                           _ptr(ws, None, "ws") if nws else None, nws, _stream(stream))
     _check(rc, "ic_attn_mass")
     return mass
 

@@ -52,9 +52,9 @@ def test_prefix_attn_refusals(ic):
 
 
 def test_attn_mass_refusals(ic):
-    call = caller(ic.lib().ic_attn_mass, "q k lse lens B Lq Lk Hq Hkv d q0 scale mass".split(),
+    call = caller(ic.lib().ic_attn_mass, "q k lse lens B Lq Lk Hq Hkv d q0 scale mass ws wsb".split(),
                   dict(q=0x1000, k=0x2000, lse=0x3000, lens=None, B=2, Lq=1, Lk=64, Hq=16, Hkv=1, d=128,
-                       q0=63, scale=0.0, mass=0x4000))
+                       q0=63, scale=0.0, mass=0x4000, ws=None, wsb=0))
     for name in ("B", "Lq", "Lk", "q0"):
         assert call(**{name: -1}) == 1
     for name in ("q", "k", "lse", "mass"):
@@ -63,7 +63,12 @@ def test_attn_mass_refusals(ic):
     assert call(lse=0x3001) == 2 and call(lens=0x3002) == 2 and call(mass=0x4002) == 2
     assert call(d=80) == 2 and call(Hkv=5) == 2
     assert call(scale=float("nan")) == 1
+    assert call(wsb=64) == 1 and call(ws=0x9008, wsb=64) == 2
+    assert call(B=70000) == 2 and call(Lk=(1 << 30) + 1) == 2 and call(Lq=(1 << 29) + 1) == 2
     assert call(B=0) == 0 and call(Lq=0) == 0 and call(Lk=0) == 0
+    assert ic.attn_mass_workspace_bytes(1, 8192, 8192, 16, 1, 128) >= 2 * 8192 * 4
+    assert ic.attn_mass_workspace_bytes(1, 1, 8192, 16, 1, 128) == 0
+    assert ic.attn_mass_workspace_bytes(1, 1, 8192, 16, 3, 128) == 0
 
 
 def test_attn_mass_sparse_refusals(ic):
