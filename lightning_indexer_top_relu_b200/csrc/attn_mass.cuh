@@ -200,17 +200,26 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             fence_barrier_init();
         }
         // columns past the row tile's last stay zero: their score is 0, their weight 2^-inf
-        for (int e = threadIdx.x; e < a.q_stages * q_bytes / 16; e += AM_THREADS)
-            reinterpret_cast<uint4*>(sq)[e] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        if (warp == 1) {
-            tmem_alloc(tmem_slot, AM_TMEM_COLS);
-            tmem_relinquish();
+        const bool padded = a.ipt * a.G < a.n_cols;
+        if (padded) {
+            for (int e = threadIdx.x; e < a.q_stages * q_bytes / 16; e += AM_THREADS)
+                reinterpret_cast<uint4*>(sq)[e] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
         }
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        const uint32_t tmem = warp_uniform(*tmem_slot);
+        // the copies start before TMEM is set up
+        if (warp == 0 && !padded) {
+            __syncwarp();
+            named_bar_arrive(4, AM_THREADS);
+        } else {
+            if (warp == 1) {
+                tmem_alloc(tmem_slot, AM_TMEM_COLS);
+                tmem_relinquish();
+            }
+            tc_fence_before();
+            named_bar(4, AM_THREADS);
+            tc_fence_after();
+        }
+        const uint32_t tmem = warp == 0 ? 0u : warp_uniform(*tmem_slot);
 
         if (warp == 0) {
             int kn = 0, qn = 0;                                 // K tiles and row tiles loaded so far
