@@ -31,6 +31,7 @@
 #include "common.cuh"
 #include "dense_attn.cuh"
 #include "prefix_attn.cuh"
+#include "sparse_attn.cuh"
 
 namespace ic {
 
@@ -423,41 +424,97 @@ struct SparseMassArgs {
 // that is not a number (or past every valid one).
 constexpr unsigned long long MASS_NAN = 1ull << 63;
 
-// One warp per slot, lane = D/32 elements of the key.
+// A warp takes 32 slots of one row at a time: S = Q K^T by m16n8k16 (heads x
+// slots), four tiles of 8 slots, with the K rows read from global memory
+// straight into the B fragments.  A dot product may sum its elements in any
+// order, so the k index of the fragments is permuted: lane (n, c) of a tile
+// reads the 16-byte chunks c of each 64 bytes of row n -- 4 lanes a whole
+// sector pair -- and each chunk feeds two k steps; the A fragments read Q in the
+// same order.  16 such loads a lane are in flight at once (bound: the latency
+// of the index and row loads for a decode step, L2 bandwidth for many rows).
+// The weights are summed over the heads by a reduce-scatter of the 8 row groups,
+// which leaves each lane one slot's sum.  Every slot's sum has the same order,
+// so slots that name one position add equal weights and their order does
+// not matter.
 template <int D>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 4)
 attn_mass_sparse_kernel(const SparseMassArgs a) {
-    constexpr int E = D / 32;
+    constexpr int NJ = D / 32;                                  // 16-byte chunks a lane and row
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, c = lane & 3;
     const long long row = blockIdx.x;
     const int i = (int)(row % a.Lq);
     const long long b = row / a.Lq;
     const int t = a.q_offset + i;
-    for (int s = blockIdx.y * 4 + warp; s < a.slots; s += gridDim.y * 4) {
-        const int id = __ldg(a.idx + row * a.slots + s);
-        if (id < 0 || id > t) {
-            if (id != -1 && lane == 0) report(DEV_ERR_BAD_INDEX);
-            continue;
+    const int32_t* irow = a.idx + row * a.slots;
+    const int stride = gridDim.y * 128;
+    int s0 = (blockIdx.y * 4 + warp) * 32;
+    int id = s0 + lane < a.slots ? __ldg(irow + s0 + lane) : -1;
+    // heads g and g + 8: queries in chunk order, -lse log2 e
+    uint4 q0[NJ], q1[NJ];
+    const bool two = a.Hq == 16;
+    const __nv_bfloat16* qrow = a.q + row * a.Hq * D;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        q0[j] = __ldg(reinterpret_cast<const uint4*>(qrow + g * D + j * 32 + c * 8));
+        q1[j] = two ? __ldg(reinterpret_cast<const uint4*>(qrow + (g + 8) * D + j * 32 + c * 8)) : make_uint4(0, 0, 0, 0);
+    }
+    const float l0 = __ldg(a.lse + row * a.Hq + g), l1 = two ? __ldg(a.lse + row * a.Hq + g + 8) : -INFINITY;
+    const float n0 = -l0 * LOG2E, n1 = -l1 * LOG2E;
+    const __nv_bfloat16* kb = a.k + b * a.Lk * D + c * 8;
+    for (; s0 < a.slots; s0 += stride) {
+        if (id != -1 && (id < 0 || id > t)) {
+            report(DEV_ERR_BAD_INDEX);
+            id = -1;
         }
-        float kf[E];
-        for (int e = 0; e < E; ++e) kf[e] = __bfloat162float(a.k[(b * a.Lk + id) * D + e * 32 + lane]);
-        float w = 0.0f;
-        for (int h = 0; h < a.Hq; ++h) {
-            float z = 0.0f;
-            for (int e = 0; e < E; ++e)
-                z = fmaf(kf[e], __bfloat162float(a.q[(row * a.Hq + h) * D + e * 32 + lane]), z);
-            for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-            const float l = a.lse[row * a.Hq + h];
-            if (l != -INFINITY) w += exp2f(fmaf(z, a.scale_log2, -l * LOG2E));
+        uint4 kr[4][NJ];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int r = __shfl_sync(0xffffffffu, id, u * 8 + g);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                kr[u][j] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(kb + (long long)r * D + j * 32))
+                                  : make_uint4(0, 0, 0, 0);
         }
-        if (lane == 0) {
-            if (a.acc == nullptr)
-                atomicAdd(a.mass + b * a.Lk + id, w);
-            else if (w >= 0.0f && w <= 2.0f * a.Hq)
-                atomicAdd(a.acc + b * a.Lk + id, __float2ull_rn(w * a.fixed_one));
-            else
-                atomicOr(a.acc + b * a.Lk + id, MASS_NAN);
+        // this lane's slot after the reduce-scatter, and the next indices
+        const int mine = __shfl_sync(0xffffffffu, id, (g >> 1) * 8 + 2 * c + (g & 1));
+        id = s0 + stride + lane < a.slots ? __ldg(irow + s0 + stride + lane) : -1;
+        float w[8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const uint32_t a0[4] = {q0[j].x, q1[j].x, q0[j].y, q1[j].y};
+                const uint32_t a1[4] = {q0[j].z, q1[j].z, q0[j].w, q1[j].w};
+                mma_bf16(z, a0, kr[u][j].x, kr[u][j].y);
+                mma_bf16(z, a1, kr[u][j].z, kr[u][j].w);
+            }
+            // heads whose row has no keys (lse -inf) add nothing
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float p0 = l0 == -INFINITY ? 0.0f : ex2_approx(fmaf(z[e], a.scale_log2, n0));
+                const float p1 = l1 == -INFINITY ? 0.0f : ex2_approx(fmaf(z[2 + e], a.scale_log2, n1));
+                w[u * 2 + e] = p0 + p1;
+            }
         }
+#pragma unroll
+        for (int h = 4; h >= 1; h >>= 1) {                      // row groups differing in bit h of g
+#pragma unroll
+            for (int x = 0; x < h; ++x) {
+                const bool up = (g & h) != 0;
+                const float send = up ? w[x] : w[x + h];
+                const float got = __shfl_xor_sync(0xffffffffu, send, h * 4);
+                w[x] = (up ? w[x + h] : w[x]) + got;
+            }
+        }
+        if (mine < 0 || mine > t) continue;
+        if (a.acc == nullptr)
+            atomicAdd(a.mass + b * a.Lk + mine, w[0]);
+        else if (w[0] >= 0.0f && w[0] <= 2.0f * a.Hq)
+            atomicAdd(a.acc + b * a.Lk + mine, __float2ull_rn(w[0] * a.fixed_one));
+        else
+            atomicOr(a.acc + b * a.Lk + mine, MASS_NAN);
     }
 }
 

@@ -366,8 +366,9 @@ int ic_attn_mass_sparse(const uint16_t* q, const uint16_t* k, const int32_t* idx
         cudaError_t e = cudaMemsetAsync(ws, 0, need, st);
         if (e != cudaSuccess) return cuda_fail(e, "attn_mass_sparse workspace clear");
     }
-    // few rows: several CTAs share a row's slots
-    const long long per_row = std::max(1LL, std::min<long long>((k_slots + 63) / 64, 8LL * sms / rows));
+    // 128 slots a CTA and pass; up to about two waves of CTAs (4 an SM), more
+    // slots a CTA beyond
+    const long long per_row = std::max(1LL, std::min<long long>({(k_slots + 127) / 128, 65535, 8LL * sms / rows}));
     const dim3 grid((unsigned)rows, (unsigned)per_row);
     if (d == 64) ic::attn_mass_sparse_kernel<64><<<grid, 128, 0, st>>>(a);
     else ic::attn_mass_sparse_kernel<128><<<grid, 128, 0, st>>>(a);
