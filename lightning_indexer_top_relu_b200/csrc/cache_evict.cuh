@@ -11,11 +11,13 @@
 //   keys in shared memory when they fit.  Three radix passes (11 + 11 + 10
 //   bits) find the key T of the last kept position: each CTA histograms its
 //   slice, and after a cluster barrier every CTA sums all slices' histograms
-//   through distributed shared memory and finds the same bin.  A counting
-//   pass gives each warp its number of keys above T and equal to T; with the
-//   counts of the CTAs before it (again through distributed shared memory)
-//   every warp knows its first output slot and writes its positions at
-//   ballot-prefix offsets, so the output is sorted without a sort.
+//   through distributed shared memory and finds the same bin.  The same scan
+//   adds up the lower slices' keys above the bin, so after the last pass a CTA
+//   knows how many positions the slices before it keep.  A counting pass gives
+//   each warp its share, and the warps write their positions at ballot-prefix
+//   offsets: the output is sorted without a sort.  Bound by the latency of
+//   its barriers and scans (four cluster barriers), not by its one read of
+//   the weights.
 //
 // Compaction (cache_gather_kernel): copies row keep[b, j] of every tensor to
 // row j.  Bound by memory bandwidth.
@@ -30,7 +32,8 @@ constexpr int EV_THREADS = 512;
 constexpr int EV_WARPS = EV_THREADS / 32;
 constexpr int EV_BINS = 2048;
 constexpr int EV_CACHE_MAX = 40960;          // keys of a slice kept in shared memory
-constexpr int EV_CLUSTER_MAX = 8;
+constexpr int EV_CLUSTER_MAX = 16;           // above 8 where the device has room for such a cluster
+constexpr int EV_BATCH = 8;                  // loads in flight a thread
 
 struct EvictArgs {
     const float* mass;       // [B, Lk]
@@ -43,10 +46,9 @@ struct EvictArgs {
 
 struct EvictSmem {
     static constexpr int OFF_HIST = 0;                               // [3][2048]
-    static constexpr int OFF_WCNT = OFF_HIST + 3 * EV_BINS * 4;      // [2][16] per-warp counts
-    static constexpr int OFF_CNT = OFF_WCNT + 2 * EV_WARPS * 4;      // gt, eq of this CTA
-    static constexpr int OFF_SCR = OFF_CNT + 16;                     // [16] scan + [4] found
-    static constexpr int OFF_KEYS = OFF_SCR + 128;
+    static constexpr int OFF_WARP = OFF_HIST + 3 * EV_BINS * 4;      // [16] u64 per-warp sums
+    static constexpr int OFF_FOUND = OFF_WARP + EV_WARPS * 8;        // bin, above, lower above, lower at
+    static constexpr int OFF_KEYS = OFF_FOUND + 16;
     static constexpr int bytes(int keys) { return OFF_KEYS + keys * 4; }
 };
 
@@ -54,16 +56,56 @@ __device__ __forceinline__ uint32_t ev_key(float f) {
     return f != f ? score_key(-INFINITY) : score_key(f);
 }
 
+// Keys e, e + step, ... below `end`: from the weights in global memory, all
+// loads first, or from the slice's copy in shared memory.
+__device__ __forceinline__ void ev_load(uint32_t (&key)[EV_BATCH], bool global, const float* src,
+                                        const uint32_t* keys, int e, int step, int end) {
+    if (global) {
+        float f[EV_BATCH];
+#pragma unroll
+        for (int u = 0; u < EV_BATCH; ++u) f[u] = e + u * step < end ? __ldg(src + e + u * step) : 0.0f;
+#pragma unroll
+        for (int u = 0; u < EV_BATCH; ++u) key[u] = ev_key(f[u]);
+    } else {
+#pragma unroll
+        for (int u = 0; u < EV_BATCH; ++u) key[u] = e + u * step < end ? keys[e + u * step] : 0u;
+    }
+}
+
+__device__ __forceinline__ void cluster_or_block_sync(int C) {
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+}
+
+// Exclusive prefix over the block of one 64-bit value a thread (two 32-bit
+// counts); `sums` is scratch of one value a warp.
+__device__ __forceinline__ unsigned long long ev_block_prefix(unsigned long long mine, unsigned long long* sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    unsigned long long s = lane < EV_WARPS ? sums[lane] : 0ull;
+#pragma unroll
+    for (int o = 1; o < EV_WARPS; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    const unsigned long long before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+    return (warp > 0 ? before : 0ull) + x - mine;
+}
+
 __global__ void __launch_bounds__(EV_THREADS)
 evict_select_kernel(const EvictArgs a) {
     using S = EvictSmem;
     extern __shared__ __align__(16) uint8_t ev_smem[];
     uint32_t* hist = reinterpret_cast<uint32_t*>(ev_smem + S::OFF_HIST);
-    uint32_t* wgt = reinterpret_cast<uint32_t*>(ev_smem + S::OFF_WCNT);
-    uint32_t* weq = wgt + EV_WARPS;
-    uint32_t* cnt = reinterpret_cast<uint32_t*>(ev_smem + S::OFF_CNT);
-    uint32_t* scr = reinterpret_cast<uint32_t*>(ev_smem + S::OFF_SCR);
-    uint32_t* found = scr + EV_WARPS;
+    unsigned long long* sums = reinterpret_cast<unsigned long long*>(ev_smem + S::OFF_WARP);
+    uint32_t* found = reinterpret_cast<uint32_t*>(ev_smem + S::OFF_FOUND);
     uint32_t* keys = reinterpret_cast<uint32_t*>(ev_smem + S::OFF_KEYS);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x, C = gridDim.x, b = blockIdx.y;      // the cluster is one row of the grid
@@ -91,65 +133,56 @@ evict_select_kernel(const EvictArgs a) {
 
     uint32_t prefix = 0;                     // the key bits fixed so far
     int remaining = kk;                      // keys still to keep among those with this prefix
+    uint32_t gt_lower = 0, eq_lower = 0;     // keys above / equal to T in the slices before this one
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int bits = pass == 2 ? 10 : 11;
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
         uint32_t* h = hist + pass * EV_BINS;
-        for (int e0 = 0; e0 < m; e0 += EV_THREADS * 8) {
-            uint32_t key[8];
-            bool in[8];
+        const bool global = pass == 0 || !a.cached;
+        for (int e0 = 0; e0 < m; e0 += EV_THREADS * EV_BATCH) {
+            uint32_t key[EV_BATCH];
+            ev_load(key, global, src, keys, e0 + tid, EV_THREADS, m);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < EV_BATCH; ++u) {
                 const int e = e0 + u * EV_THREADS + tid;
-                in[u] = e < m;
-                if (pass == 0 || !a.cached) key[u] = in[u] ? ev_key(__ldg(src + e)) : 0u;
-                else key[u] = in[u] ? keys[e] : 0u;
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int e = e0 + u * EV_THREADS + tid;
-                if (pass == 0 && a.cached && in[u]) keys[e] = key[u];
-                const bool on = in[u] && (pass == 0 || (key[u] >> (shift + bits)) == prefix);
-                const uint32_t bin = (key[u] >> shift) & ((1u << bits) - 1u);
-                // one add for a warp whose keys all fall in one bin (equal weights)
-                const uint32_t who = __ballot_sync(0xffffffffu, on);
-                if (who == 0u) continue;
-                const int first = __ffs(who) - 1;
-                const uint32_t b0 = __shfl_sync(0xffffffffu, bin, first);
-                if (__all_sync(0xffffffffu, !on || bin == b0)) {
-                    if (lane == first) atomicAdd(h + b0, (uint32_t)__popc(who));
-                } else if (on) {
-                    atomicAdd(h + bin, 1u);
+                if (e < m) {
+                    if (pass == 0 && a.cached) keys[e] = key[u];
+                    // (no vote on equal bins first: adds of one constant to one address combine)
+                    if (pass == 0 || (key[u] >> (shift + bits)) == prefix)
+                        atomicAdd(h + ((key[u] >> shift) & ((1u << bits) - 1u)), 1u);
                 }
             }
         }
-        cluster_sync();
-        // every CTA sums all slices' bins, highest first: thread t has bins [2044 - 4t, 2048 - 4t)
-        uint32_t c[4] = {0, 0, 0, 0};
+        cluster_or_block_sync(C);
+        // every CTA sums all slices' bins, highest first: thread t has bins
+        // [2044 - 4t, 2048 - 4t); high word: the slices before this one alone
+        unsigned long long c[4] = {0, 0, 0, 0};
         const int bin0 = EV_BINS - 4 - 4 * tid;
-        for (int r = 0; r < C; ++r) {
-            const uint4 v = ld_dsmem_v4(smem_u32(h + bin0), (uint32_t)r);
-            c[0] += v.w;
-            c[1] += v.z;
-            c[2] += v.y;
-            c[3] += v.x;
-        }
-        const uint32_t mine = c[0] + c[1] + c[2] + c[3];
-        uint32_t x = mine;
+        for (int r0 = 0; r0 < C; r0 += 8) {
+            uint4 v[8];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+            for (int r = 0; r < 8; ++r)
+                v[r] = r0 + r < C ? (C > 1 ? ld_dsmem_v4(smem_u32(h + bin0), (uint32_t)(r0 + r))
+                                           : *reinterpret_cast<const uint4*>(h + bin0))
+                                  : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const unsigned long long one = r0 + r < rank ? (1ull << 32) + 1 : 1ull;
+                c[0] += v[r].w * one;
+                c[1] += v[r].z * one;
+                c[2] += v[r].y * one;
+                c[3] += v[r].x * one;
+            }
         }
-        if (lane == 31) scr[warp] = x;
-        __syncthreads();
-        uint32_t above = x - mine;
-        for (int w = 0; w < warp; ++w) above += scr[w];
+        unsigned long long above = ev_block_prefix(c[0] + c[1] + c[2] + c[3], sums);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            if (above < (uint32_t)remaining && above + c[u] >= (uint32_t)remaining) {
+            if ((uint32_t)above < (uint32_t)remaining && (uint32_t)above + (uint32_t)c[u] >= (uint32_t)remaining) {
                 found[0] = (uint32_t)(bin0 + 3 - u);
-                found[1] = above;
+                found[1] = (uint32_t)above;
+                found[2] = (uint32_t)(above >> 32);
+                found[3] = (uint32_t)(c[u] >> 32);
             }
             above += c[u];
         }
@@ -157,6 +190,8 @@ evict_select_kernel(const EvictArgs a) {
         if (remaining > 0) {                 // kk == 0 keeps none: T stays above every key
             prefix = (prefix << bits) | found[0];
             remaining -= (int)found[1];
+            gt_lower += found[2];
+            eq_lower = found[3];
         }
         __syncthreads();
     }
@@ -167,57 +202,40 @@ evict_select_kernel(const EvictArgs a) {
     const int seg = ((m + EV_WARPS - 1) / EV_WARPS + 31) / 32 * 32;
     const int w0 = min(warp * seg, m), w1 = min(w0 + seg, m);
     uint32_t gt = 0, eq = 0;
-    for (int e = w0 + lane; e < w1; e += 32) {
-        const uint32_t key = a.cached ? keys[e] : ev_key(__ldg(src + e));
-        gt += key > T;
-        eq += key == T;
-    }
+    for (int e0 = w0; e0 < w1; e0 += 32 * EV_BATCH) {
+        uint32_t key[EV_BATCH];
+        ev_load(key, !a.cached, src, keys, e0 + lane, 32, w1);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        gt += __shfl_xor_sync(0xffffffffu, gt, o);
-        eq += __shfl_xor_sync(0xffffffffu, eq, o);
-    }
-    if (lane == 0) {
-        wgt[warp] = gt;
-        weq[warp] = eq;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        uint32_t g = 0, q = 0;
-        for (int w = 0; w < EV_WARPS; ++w) {
-            g += wgt[w];
-            q += weq[w];
+        for (int u = 0; u < EV_BATCH; ++u) {
+            const bool in = e0 + u * 32 + lane < w1;
+            gt += in && key[u] > T;
+            eq += in && key[u] == T;
         }
-        cnt[0] = g;
-        cnt[1] = q;
     }
-    cluster_sync();
-    uint32_t gt_before = 0, eq_before = 0;
-    for (int r = 0; r < rank; ++r) {
-        const uint4 v = ld_dsmem_v4(smem_u32(cnt), (uint32_t)r);
-        gt_before += v.x;
-        eq_before += v.y;
-    }
-    for (int w = 0; w < warp; ++w) {
-        gt_before += wgt[w];
-        eq_before += weq[w];
-    }
+    // a thread's share of the block's counts; a warp's first lane has the sum before it
+    const unsigned long long before = ev_block_prefix((unsigned long long)eq << 32 | gt, sums);
+    uint32_t gt_before = gt_lower + (uint32_t)__shfl_sync(0xffffffffu, before, 0);
+    uint32_t eq_before = eq_lower + (uint32_t)(__shfl_sync(0xffffffffu, before, 0) >> 32);
     const uint32_t lt = (1u << lane) - 1u;
-    for (int e0 = w0; e0 < w1; e0 += 32) {
-        const int e = e0 + lane;
-        const uint32_t key = e < w1 ? (a.cached ? keys[e] : ev_key(__ldg(src + e))) : 0u;
-        const uint32_t mg = __ballot_sync(0xffffffffu, e < w1 && key > T);
-        const uint32_t me = __ballot_sync(0xffffffffu, e < w1 && key == T);
-        const uint32_t eqi = eq_before + (uint32_t)__popc(me & lt);      // equal keys before this one
-        const bool take_eq = ((me >> lane) & 1u) && eqi < (uint32_t)need;
-        if (((mg >> lane) & 1u) || take_eq) {
-            const uint32_t slot = gt_before + (uint32_t)__popc(mg & lt) + min(eqi, (uint32_t)need);
-            keep[a.n_sink + slot] = a.n_sink + lo + e;
+    for (int e0 = w0; e0 < w1; e0 += 32 * EV_BATCH) {
+        uint32_t key[EV_BATCH];
+        ev_load(key, !a.cached, src, keys, e0 + lane, 32, w1);
+#pragma unroll
+        for (int u = 0; u < EV_BATCH; ++u) {
+            const int e = e0 + u * 32 + lane;
+            const uint32_t mg = __ballot_sync(0xffffffffu, e < w1 && key[u] > T);
+            const uint32_t me = __ballot_sync(0xffffffffu, e < w1 && key[u] == T);
+            const uint32_t eqi = eq_before + (uint32_t)__popc(me & lt);  // equal keys before this one
+            const bool take_eq = ((me >> lane) & 1u) && eqi < (uint32_t)need;
+            if (((mg >> lane) & 1u) || take_eq) {
+                const uint32_t slot = gt_before + (uint32_t)__popc(mg & lt) + min(eqi, (uint32_t)need);
+                keep[a.n_sink + slot] = a.n_sink + lo + e;
+            }
+            gt_before += (uint32_t)__popc(mg);
+            eq_before += (uint32_t)__popc(me);
         }
-        gt_before += (uint32_t)__popc(mg);
-        eq_before += (uint32_t)__popc(me);
     }
-    cluster_sync();                       // no CTA leaves while another may read its shared memory
+    if (C > 1) cluster_sync();               // no CTA leaves while another may read its shared memory
 }
 
 // ---------------------------------------------------------------- compaction

@@ -70,11 +70,14 @@ MassGeom mass_geom(int B, int Lq, int Lk, int Hq, int Hkv, int d, int sms) {
     return g;
 }
 
-// CTAs per sequence of the eviction select: enough that a slice fits in
-// shared memory, and about 4K positions each for short caches.
-int evict_cluster(int Lk) {
+// CTAs (one cluster) per sequence of the eviction select: slices of about 4K
+// positions while that leaves SMs idle, and in any case slices that fit in shared memory where
+// clusters are large enough.
+int evict_cluster(int B, int Lk, int sms, int most) {
     int c = 1;
-    while (c < ic::EV_CLUSTER_MAX && (Lk + c - 1) / c > 4096) c *= 2;
+    while (c < most && (Lk + c - 1) / c > 4096 &&
+           ((long long)B * c < 2 * sms || (Lk + c - 1) / c > ic::EV_CACHE_MAX))
+        c *= 2;
     return c;
 }
 
@@ -402,7 +405,7 @@ int ic_evict_select(const float* mass, const int32_t* lens, int B, int Lk, int n
     a.keep = keep;
     a.new_lens = new_lens;
     a.B = B; a.Lk = Lk; a.n_keep = n_keep; a.n_sink = n_sink; a.n_recent = n_recent;
-    const int C = evict_cluster(Lk);
+    const int C = evict_cluster(B, Lk, sms, g_evict_cluster[dev]);
     const int per = (Lk + C - 1) / C;
     a.cached = per <= ic::EV_CACHE_MAX ? 1 : 0;
     cudaLaunchConfig_t cfg = {};

@@ -76,6 +76,8 @@ int g_sms[MAX_DEV];
 bool g_attr_done[MAX_DEV];
 // 8-CTA clusters of the gather kernel fit on the device (checked at setup)
 bool g_attn_cluster[MAX_DEV];
+// largest cluster of the eviction select that fits on the device
+int g_evict_cluster[MAX_DEV];
 
 int device_setup(int* dev_out, int* sms_out);
 
@@ -366,6 +368,26 @@ bool attn_cluster_fits() {
     cfg.numAttrs = 1;
     int n = 0;
     return cudaOccupancyMaxActiveClusters(&n, ic::sparse_attn_kernel<D>, &cfg) == cudaSuccess && n > 0;
+}
+
+// Whether clusters of c CTAs of the eviction select with full slices fit.
+bool evict_cluster_fits(int c) {
+    if (c > 8 && cudaFuncSetAttribute(ic::evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                     cudaSuccess)
+        return false;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c, 1, 1);
+    cfg.blockDim = dim3(ic::EV_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = ic::EvictSmem::bytes(ic::EV_CACHE_MAX);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)c;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, ic::evict_select_kernel, &cfg) == cudaSuccess && n > 0;
 }
 
 bool attn_cluster_available() {
@@ -817,6 +839,8 @@ int device_setup(int* dev_out, int* sms_out) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
         g_attn_cluster[dev] = attn_cluster_fits<64>() && attn_cluster_fits<128>();
+        g_evict_cluster[dev] = evict_cluster_fits(ic::EV_CLUSTER_MAX) ? ic::EV_CLUSTER_MAX
+                               : evict_cluster_fits(8) ? 8 : 1;
         cudaGetLastError();                         // a refused query only disables clusters
         g_sms[dev] = sms;
         g_attr_done[dev] = true;
