@@ -8,16 +8,17 @@
 // as IEEE floats, NaN as -inf.  Exact.
 //   One thread-block cluster per sequence; each of its CTAs owns a contiguous
 //   slice of the middle positions and holds their order-preserving 32-bit
-//   keys in shared memory when they fit.  Three radix passes (11 + 11 + 10
-//   bits) find the key T of the last kept position: each CTA histograms its
+//   keys in shared memory when they fit.  Four radix passes of 8 bits find
+//   the key T of the last kept position: each CTA histograms its
 //   slice, and after a cluster barrier every CTA sums all slices' histograms
 //   through distributed shared memory and finds the same bin.  The same scan
 //   adds up the lower slices' keys above the bin, so after the last pass a CTA
 //   knows how many positions the slices before it keep.  A counting pass gives
 //   each warp its share, and the warps write their positions at ballot-prefix
 //   offsets: the output is sorted without a sort.  Bound by the latency of
-//   its barriers and scans (four cluster barriers), not by its one read of
-//   the weights.
+//   its barriers and scans (five cluster barriers), not by its one read of
+//   the weights.  (Three passes of 11 + 11 + 10 bits: two 500K caches took 51
+//   us, most of it reading 2048 bins of 16 slices in every CTA.)
 //
 // Compaction (cache_gather_kernel): copies row keep[b, j] of every tensor to
 // row j.  Bound by memory bandwidth.
@@ -30,7 +31,7 @@ namespace ic {
 
 constexpr int EV_THREADS = 512;
 constexpr int EV_WARPS = EV_THREADS / 32;
-constexpr int EV_BINS = 2048;
+constexpr int EV_BINS = 256;                 // 8 bits a pass
 constexpr int EV_CACHE_MAX = 40960;          // keys of a slice kept in shared memory
 constexpr int EV_CLUSTER_MAX = 16;           // above 8 where the device has room for such a cluster
 constexpr int EV_BATCH = 8;                  // loads in flight a thread
@@ -45,8 +46,8 @@ struct EvictArgs {
 };
 
 struct EvictSmem {
-    static constexpr int OFF_HIST = 0;                               // [3][2048]
-    static constexpr int OFF_WARP = OFF_HIST + 3 * EV_BINS * 4;      // [16] u64 per-warp sums
+    static constexpr int OFF_HIST = 0;                               // [4][256]
+    static constexpr int OFF_WARP = OFF_HIST + 4 * EV_BINS * 4;      // [16] u64 per-warp sums
     static constexpr int OFF_FOUND = OFF_WARP + EV_WARPS * 8;        // bin, above, lower above, lower at
     static constexpr int OFF_KEYS = OFF_FOUND + 16;
     static constexpr int bytes(int keys) { return OFF_KEYS + keys * 4; }
@@ -56,19 +57,20 @@ __device__ __forceinline__ uint32_t ev_key(float f) {
     return f != f ? score_key(-INFINITY) : score_key(f);
 }
 
-// Keys e, e + step, ... below `end`: from the weights in global memory, all
-// loads first, or from the slice's copy in shared memory.
+// Keys e, e + step, ... (past the end: the last one again): from the weights in
+// global memory, all loads first, or from the slice's copy in shared memory.
+// Loads behind a bounds branch ran one after the other.
 __device__ __forceinline__ void ev_load(uint32_t (&key)[EV_BATCH], bool global, const float* src,
                                         const uint32_t* keys, int e, int step, int end) {
     if (global) {
         float f[EV_BATCH];
 #pragma unroll
-        for (int u = 0; u < EV_BATCH; ++u) f[u] = e + u * step < end ? __ldg(src + e + u * step) : 0.0f;
+        for (int u = 0; u < EV_BATCH; ++u) f[u] = __ldg(src + min(e + u * step, end - 1));
 #pragma unroll
         for (int u = 0; u < EV_BATCH; ++u) key[u] = ev_key(f[u]);
     } else {
 #pragma unroll
-        for (int u = 0; u < EV_BATCH; ++u) key[u] = e + u * step < end ? keys[e + u * step] : 0u;
+        for (int u = 0; u < EV_BATCH; ++u) key[u] = keys[min(e + u * step, end - 1)];
     }
 }
 
@@ -128,16 +130,15 @@ evict_select_kernel(const EvictArgs a) {
         for (int j = tid; j < a.n_sink; j += EV_THREADS) keep[j] = j;
     if (rank == C - 1)
         for (int j = tid; j < a.n_recent; j += EV_THREADS) keep[a.n_keep - a.n_recent + j] = n - a.n_recent + j;
-    for (int e = tid; e < 3 * EV_BINS; e += EV_THREADS) hist[e] = 0u;
+    for (int e = tid; e < 4 * EV_BINS; e += EV_THREADS) hist[e] = 0u;
     __syncthreads();
 
     uint32_t prefix = 0;                     // the key bits fixed so far
     int remaining = kk;                      // keys still to keep among those with this prefix
     uint32_t gt_lower = 0, eq_lower = 0;     // keys above / equal to T in the slices before this one
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int bits = pass == 2 ? 10 : 11;
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
         uint32_t* h = hist + pass * EV_BINS;
         const bool global = pass == 0 || !a.cached;
         for (int e0 = 0; e0 < m; e0 += EV_THREADS * EV_BATCH) {
@@ -149,46 +150,41 @@ evict_select_kernel(const EvictArgs a) {
                 if (e < m) {
                     if (pass == 0 && a.cached) keys[e] = key[u];
                     // (no vote on equal bins first: adds of one constant to one address combine)
-                    if (pass == 0 || (key[u] >> (shift + bits)) == prefix)
-                        atomicAdd(h + ((key[u] >> shift) & ((1u << bits) - 1u)), 1u);
+                    if (pass == 0 || (key[u] >> shift >> 8) == prefix) atomicAdd(h + ((key[u] >> shift) & 255u), 1u);
                 }
             }
         }
         cluster_or_block_sync(C);
-        // every CTA sums all slices' bins, highest first: thread t has bins
-        // [2044 - 4t, 2048 - 4t); high word: the slices before this one alone
-        unsigned long long c[4] = {0, 0, 0, 0};
-        const int bin0 = EV_BINS - 4 - 4 * tid;
-        for (int r0 = 0; r0 < C; r0 += 8) {
-            uint4 v[8];
+        // every CTA sums all slices' bins, highest first: thread t has bin 255 - t;
+        // `lower`: the slices before this one alone
+        uint32_t all = 0, lower = 0;
+        const uint32_t* bin = h + (EV_BINS - 1 - tid);
+        if (tid < EV_BINS) {
+            if (C == 1) {
+                all = *bin;
+            } else {
+                for (int r0 = 0; r0 < C; r0 += 8) {
+                    uint32_t v[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-                v[r] = r0 + r < C ? (C > 1 ? ld_dsmem_v4(smem_u32(h + bin0), (uint32_t)(r0 + r))
-                                           : *reinterpret_cast<const uint4*>(h + bin0))
-                                  : make_uint4(0, 0, 0, 0);
+                    for (int r = 0; r < 8; ++r) v[r] = ld_dsmem_u32(smem_u32(bin), (uint32_t)min(r0 + r, C - 1));
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const unsigned long long one = r0 + r < rank ? (1ull << 32) + 1 : 1ull;
-                c[0] += v[r].w * one;
-                c[1] += v[r].z * one;
-                c[2] += v[r].y * one;
-                c[3] += v[r].x * one;
+                    for (int r = 0; r < 8; ++r) {
+                        if (r0 + r < C) all += v[r];
+                        if (r0 + r < rank) lower += v[r];
+                    }
+                }
             }
         }
-        unsigned long long above = ev_block_prefix(c[0] + c[1] + c[2] + c[3], sums);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if ((uint32_t)above < (uint32_t)remaining && (uint32_t)above + (uint32_t)c[u] >= (uint32_t)remaining) {
-                found[0] = (uint32_t)(bin0 + 3 - u);
-                found[1] = (uint32_t)above;
-                found[2] = (uint32_t)(above >> 32);
-                found[3] = (uint32_t)(c[u] >> 32);
-            }
-            above += c[u];
+        const unsigned long long above = ev_block_prefix((unsigned long long)lower << 32 | all, sums);
+        if ((uint32_t)above < (uint32_t)remaining && (uint32_t)above + all >= (uint32_t)remaining) {
+            found[0] = (uint32_t)(EV_BINS - 1 - tid);
+            found[1] = (uint32_t)above;
+            found[2] = (uint32_t)(above >> 32);
+            found[3] = lower;
         }
         __syncthreads();
         if (remaining > 0) {                 // kk == 0 keeps none: T stays above every key
-            prefix = (prefix << bits) | found[0];
+            prefix = (prefix << 8) | found[0];
             remaining -= (int)found[1];
             gt_lower += found[2];
             eq_lower = found[3];
