@@ -10,6 +10,7 @@ non-zero status.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Sequence
 
@@ -146,7 +147,7 @@ _lib.ic_attn_mass_sparse_workspace_bytes.argtypes = [_I, _I, _I]
 _lib.ic_evict_select.restype = _I
 _lib.ic_evict_select.argtypes = [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P]
 _lib.ic_cache_gather.restype = _I
-_lib.ic_cache_gather.argtypes = [_P, _I, _I, _I, _I, _I, ctypes.POINTER(ICCacheCopy), _P]
+_lib.ic_cache_gather.argtypes = [_P, _I, _I, _I, _I, _I, _P, _P]
 
 
 def lib() -> ctypes.CDLL:
@@ -181,7 +182,7 @@ def _expect(t: Optional[torch.Tensor], shape, name: str) -> None:
     """A caller tensor must have exactly the shape the call derives from its
     leading operand: the C layer sees only pointers and sizes, so a smaller
     tensor would let a kernel read or write past its end."""
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -209,6 +210,39 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
+
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, dev: int) -> Optional[int]:
+    """_stream without building a Stream object for the current one (3 us of a
+    decode step's call)."""
+    if stream is None and _current_raw_stream is not None:
+        return _current_raw_stream(dev)
+    return _stream(stream)
+
+
+def _dev(t: torch.Tensor, name: str) -> int:
+    """The current device's index; a leading operand elsewhere fails as in _ptr."""
+    if t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch.cuda.current_device()
+
+
+def _at(t: Optional[torch.Tensor], dev: int, dtype, name: str) -> Optional[int]:
+    """_ptr for a call that has looked the current device up."""
+    if t is None:
+        return None
+    if t.get_device() == dev and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, dtype, name)
+
+
+def _ws_at(ws: Optional[torch.Tensor], dev: int):
+    """(pointer, bytes) of a workspace; (None, 0) for none or an empty one."""
+    nws = 0 if ws is None else ws.numel() * ws.element_size()
+    return (_at(ws, dev, None, "ws"), nws) if nws else (None, 0)
 
 
 def get_last_device_error(stream=None) -> int:
@@ -410,14 +444,13 @@ def prefix_attn(q, k_prefix, v_prefix, k=None, v=None, lens=None, scale: float =
     if ws is None:
         nbytes = prefix_attn_workspace_bytes(B, Lq, P, S, Hq, Hkv, d)
         ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8) if nbytes else None
-    nws = 0 if ws is None else ws.numel() * ws.element_size()
-    rc = _lib.ic_prefix_attn(_ptr(q, torch.bfloat16, "q"),
-                             _ptr(k_prefix, torch.bfloat16, "k_prefix"),
-                             _ptr(v_prefix, torch.bfloat16, "v_prefix"),
-                             _ptr(k, torch.bfloat16, "k"), _ptr(v, torch.bfloat16, "v"),
-                             _ptr(lens, torch.int32, "lens"), B, Lq, P, S, Hq, Hkv, d, float(scale),
-                             _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"),
-                             _ptr(ws, None, "ws") if nws else None, nws, _stream(stream))
+    dev, bf = _dev(q, "q"), torch.bfloat16
+    rc = _lib.ic_prefix_attn(_at(q, dev, bf, "q"), _at(k_prefix, dev, bf, "k_prefix"),
+                             _at(v_prefix, dev, bf, "v_prefix"), _at(k, dev, bf, "k"),
+                             _at(v, dev, bf, "v"), _at(lens, dev, torch.int32, "lens"), B, Lq, P, S,
+                             Hq, Hkv, d, float(scale), _at(out, dev, bf, "out"),
+                             _at(lse, dev, torch.float32, "lse"), *_ws_at(ws, dev),
+                             _raw_stream(stream, dev))
     _check(rc, "ic_prefix_attn")
     return out, lse
 
@@ -441,12 +474,11 @@ def attn_mass(q, k, lse, mass, lens=None, q_offset: int = 0, scale: float = 0.0,
     if ws is None:
         nbytes = attn_mass_workspace_bytes(B, Lq, Lk, Hq, Hkv, d)
         ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8) if nbytes else None
-    nws = 0 if ws is None else ws.numel() * ws.element_size()
-    rc = _lib.ic_attn_mass(_ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"),
-                           _ptr(lse, torch.float32, "lse"), _ptr(lens, torch.int32, "lens"), B, Lq,
-                           Lk, Hq, Hkv, d, q_offset, float(scale),
-                           _ptr(mass, torch.float32, "mass"),
-                           _ptr(ws, None, "ws") if nws else None, nws, _stream(stream))
+    dev, bf, f32 = _dev(q, "q"), torch.bfloat16, torch.float32
+    rc = _lib.ic_attn_mass(_at(q, dev, bf, "q"), _at(k, dev, bf, "k"), _at(lse, dev, f32, "lse"),
+                           _at(lens, dev, torch.int32, "lens"), B, Lq, Lk, Hq, Hkv, d, q_offset,
+                           float(scale), _at(mass, dev, f32, "mass"), *_ws_at(ws, dev),
+                           _raw_stream(stream, dev))
     _check(rc, "ic_attn_mass")
     return mass
 
@@ -468,12 +500,12 @@ def attn_mass_sparse(q, k, idx, lse, mass, q_offset: int = 0, scale: float = 0.0
     if ws is None:
         nbytes = attn_mass_sparse_workspace_bytes(B, Lq, Lk)
         ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8) if nbytes else None
-    nws = 0 if ws is None else ws.numel() * ws.element_size()
-    rc = _lib.ic_attn_mass_sparse(_ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"),
-                                  _ptr(idx, torch.int32, "idx"), _ptr(lse, torch.float32, "lse"), B,
+    dev, bf, f32 = _dev(q, "q"), torch.bfloat16, torch.float32
+    rc = _lib.ic_attn_mass_sparse(_at(q, dev, bf, "q"), _at(k, dev, bf, "k"),
+                                  _at(idx, dev, torch.int32, "idx"), _at(lse, dev, f32, "lse"), B,
                                   Lq, Lk, Hq, Hkv, d, kslots, q_offset, float(scale),
-                                  _ptr(mass, torch.float32, "mass"),
-                                  _ptr(ws, None, "ws") if nws else None, nws, _stream(stream))
+                                  _at(mass, dev, f32, "mass"), *_ws_at(ws, dev),
+                                  _raw_stream(stream, dev))
     _check(rc, "ic_attn_mass_sparse")
     return mass
 
@@ -492,9 +524,10 @@ def evict_select(mass, n_keep: int, lens=None, n_sink: int = 0, n_recent: int = 
         new_lens = torch.empty(B, device=mass.device, dtype=torch.int32)
     _expect(keep, (B, n_keep), "keep")
     _expect(new_lens, (B,), "new_lens")
-    rc = _lib.ic_evict_select(_ptr(mass, torch.float32, "mass"), _ptr(lens, torch.int32, "lens"), B,
-                              Lk, n_keep, n_sink, n_recent, _ptr(keep, torch.int32, "keep"),
-                              _ptr(new_lens, torch.int32, "new_lens"), _stream(stream))
+    dev, i32 = _dev(mass, "mass"), torch.int32
+    rc = _lib.ic_evict_select(_at(mass, dev, torch.float32, "mass"), _at(lens, dev, i32, "lens"), B,
+                              Lk, n_keep, n_sink, n_recent, _at(keep, dev, i32, "keep"),
+                              _at(new_lens, dev, i32, "new_lens"), _raw_stream(stream, dev))
     _check(rc, "ic_evict_select")
     return keep, new_lens
 
@@ -509,18 +542,20 @@ def cache_gather(keep, srcs: Sequence[torch.Tensor], dsts: Sequence[torch.Tensor
         raise ValueError(f"{len(srcs)} sources, {len(dsts)} destinations")
     Lk = srcs[0].shape[1] if srcs and srcs[0].dim() >= 2 else 0
     Lk_dst = dsts[0].shape[1] if dsts and dsts[0].dim() >= 2 else n_keep
-    copies = (ICCacheCopy * max(len(srcs), 1))()
-    for x, (s, d) in enumerate(zip(srcs, dsts)):
-        _expect(s, (B, Lk) + tuple(s.shape[2:]), f"source {x}")
-        _expect(d, (B, Lk_dst) + tuple(s.shape[2:]), f"destination {x}")
-    for x, (s, d) in enumerate(zip(srcs, dsts)):
-        row = s.element_size()
-        for n in s.shape[2:]:
-            row *= n
-        copies[x] = ICCacheCopy(_ptr(s, None, f"source {x}"), _ptr(d, s.dtype, f"destination {x}"),
-                                row)
-    rc = _lib.ic_cache_gather(_ptr(keep, torch.int32, "keep"), B, Lk, n_keep, Lk_dst, len(srcs),
-                              copies, _stream(stream))
+    shapes = [(s.shape, d.shape) for s, d in zip(srcs, dsts)]
+    for x, (ss, ds) in enumerate(shapes):
+        if len(ss) < 2 or ss[0] != B or ss[1] != Lk:
+            _expect(srcs[x], (B, Lk) + ss[2:], f"source {x}")
+        if len(ds) != len(ss) or ds[0] != B or ds[1] != Lk_dst or ds[2:] != ss[2:]:
+            _expect(dsts[x], (B, Lk_dst) + ss[2:], f"destination {x}")
+    dev = _dev(keep, "keep")
+    flat = []                                     # ic_cache_copy fields, tensor by tensor
+    for s, d, (ss, _) in zip(srcs, dsts, shapes):
+        flat += (_at(s, dev, None, "source"), _at(d, dev, s.dtype, "destination"),
+                 math.prod(ss[2:]) * s.element_size())
+    rc = _lib.ic_cache_gather(_at(keep, dev, torch.int32, "keep"), B, Lk, n_keep, Lk_dst, len(srcs),
+                              (ctypes.c_longlong * max(len(flat), 1))(*flat),
+                              _raw_stream(stream, dev))
     _check(rc, "ic_cache_gather")
     return dsts
 
