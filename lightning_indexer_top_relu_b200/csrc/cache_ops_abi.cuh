@@ -97,6 +97,7 @@ struct PrefixGeom {
     int o_row_units = 0, o_splits = 0, o_tps = 0, o_streams = 0;
     int slots = 0;
     long long n_prefix = 0, n_own = 0;
+    int ranks = 0;                 // > 0: the own caches and the merge in a kernel of clusters of so many CTAs
     size_t ws_bytes = 0;
 };
 
@@ -111,7 +112,22 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
     const int T = ic::PA_KEYS, R = ic::PA_ROWS, G = Hq / Hkv;
     const long long rp = (long long)B * Lq * G, ro = (long long)Lq * G;
     const int p_nt = (P + T - 1) / T, o_nt = std::max(1, (S + T - 1) / T);
-    const bool has_p = P > 0, has_o = S > 0 || P == 0;        // no key at all: the own units write zeros
+    // few rows a sequence: the own caches are not units of this kernel
+    const bool merge_kernel = ro <= ic::PO_MAX_ROWS && (long long)B * Hkv <= MAX_GRID_X / 8;
+    const bool has_p = P > 0, has_o = !merge_kernel && (S > 0 || P == 0);   // no key at all: the own units write zeros
+    // clusters for about four CTAs an SM, with at least 64 keys a key stream
+    // or 64 partial rows a CTA
+    auto cluster = [&](long long slots) {
+        const long long units = (long long)B * Hkv;
+        const int kw = ro <= 16 ? 4 : ro <= 32 ? 2 : 1;
+        int r = 1;
+        while (r < 8 && units * r * 2 <= 4LL * sms && (S / (r * 2 * kw) >= 64 || ro * slots >= 128LL * r)) r *= 2;
+        return r;
+    };
+    if (merge_kernel && !has_p) {
+        g.ranks = cluster(0);
+        return g;
+    }
     g.shared = rp > R;
     const int per_step = g.shared ? 2 : 1;
     if (has_p) g.p_row_units = (int)((rp + R * per_step - 1) / (R * per_step));
@@ -130,7 +146,7 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
         const double n = (double)n_pu * p_sp + (double)n_ou * o_sp;
         const double unit = 6.0 + std::max(has_p ? p_tps * per_step : 0, has_o ? 2 * o_tps : 0);
         double est = n <= sms ? unit : std::max(unit, (p_work + o_work + 6.0 * n) / sms + 0.5 * unit);
-        if (slots > 1) est += merge * slots;
+        if (slots > 1 || merge_kernel) est += merge * slots;
         if (n < 2147483647.0 && (best < 0.0 || est < best)) {
             best = est;
             g.p_tps = p_tps; g.o_tps = o_tps;
@@ -140,9 +156,10 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
         }
         if (s >= s_max) break;
     }
+    if (merge_kernel) g.ranks = cluster(g.slots);
     g.n_prefix = n_pu * g.p_splits;
     g.n_own = n_ou * g.o_splits;
-    if (g.slots > 1) g.ws_bytes = (size_t)B * Lq * Hq * g.slots * (d + 1) * sizeof(float);
+    if (g.slots > 1 || merge_kernel) g.ws_bytes = (size_t)B * Lq * Hq * g.slots * (d + 1) * sizeof(float);
     return g;
 }
 
@@ -165,6 +182,50 @@ int make_tmap(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, 
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(IC_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return IC_OK;
+}
+
+// The second kernel: own caches and merge.  After a prefix kernel it is launched as its
+// programmatic dependent.
+int launch_prefix_own(const PrefixGeom& g, const ic::PrefixAttnArgs& p, const uint16_t* k, const uint16_t* v, int d,
+                      bool dependent, cudaStream_t st) {
+    ic::PrefixOwnArgs a{};
+    a.q = p.q;
+    a.k = reinterpret_cast<const __nv_bfloat16*>(k);
+    a.v = reinterpret_cast<const __nv_bfloat16*>(v);
+    a.lens = p.lens;
+    a.out = p.out;
+    a.lse = p.lse;
+    a.part_o = p.part_o;
+    a.part_lse = p.part_lse;
+    a.slots = dependent ? g.slots : 0;
+    a.B = p.B; a.Lq = p.Lq; a.S = p.S; a.Hq = p.Hq; a.Hkv = p.Hkv; a.G = p.G;
+    a.ranks = g.ranks;
+    a.scale_log2 = p.scale_log2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(g.ranks * p.B * p.Hkv));
+    cfg.blockDim = dim3(ic::PO_THREADS);
+    cfg.dynamicSmemBytes = d == 64 ? ic::OwnSmem<64>::BYTES : ic::OwnSmem<128>::BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)g.ranks;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = dependent ? 2 : 1;
+    const int rows = p.Lq * p.G;
+    cudaError_t e;
+    if (d == 64)
+        e = rows <= 16   ? cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<64, 1>, a)
+            : rows <= 32 ? cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<64, 2>, a)
+                         : cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<64, 4>, a);
+    else
+        e = rows <= 16   ? cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<128, 1>, a)
+            : rows <= 32 ? cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<128, 2>, a)
+                         : cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<128, 4>, a);
+    return launched(e, "prefix_attn own launch");
 }
 
 }  // namespace
@@ -239,11 +300,15 @@ int ic_prefix_attn(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* 
     a.scale_log2 = scale_log2_of(scale, d);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)(g.n_prefix + g.n_own);
-    if (d == 64)
+    a.to_parts = g.ranks > 0 || g.slots > 1 ? 1 : 0;
+    if (grid == 0) {
+        // no prefix
+    } else if (d == 64)
         ic::prefix_attn_kernel<64><<<grid, ic::PA_THREADS, ic::PrefixSmem<64>::ALLOC, st>>>(tkp, tvp, tk, tv, a);
     else
         ic::prefix_attn_kernel<128><<<grid, ic::PA_THREADS, ic::PrefixSmem<128>::ALLOC, st>>>(tkp, tvp, tk, tv, a);
-    if (launched(cudaGetLastError(), "prefix_attn launch")) return IC_ERR_CUDA;
+    if (grid > 0 && launched(cudaGetLastError(), "prefix_attn launch")) return IC_ERR_CUDA;
+    if (g.ranks > 0) return launch_prefix_own(g, a, k, v, d, grid > 0, st);
     if (g.slots == 1) return IC_OK;
     const bool wide = g.slots > 8;
     const unsigned cg = (unsigned)(wide ? rows : (rows + 3) / 4);

@@ -25,6 +25,7 @@
 #include "index_overlap.cuh"
 #include "indexer_scores.cuh"
 #include "prefix_attn.cuh"
+#include "prefix_own.cuh"
 #include "sparse_attn.cuh"
 #include "topk_select.cuh"
 
@@ -388,6 +389,14 @@ bool evict_cluster_fits(int c) {
     cfg.numAttrs = 1;
     int n = 0;
     return cudaOccupancyMaxActiveClusters(&n, ic::evict_select_kernel, &cfg) == cudaSuccess && n > 0;
+}
+
+template <int D>
+void set_own_attr() {
+    const auto max = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaFuncSetAttribute(ic::prefix_own_kernel<D, 1>, max, ic::OwnSmem<D>::BYTES);
+    cudaFuncSetAttribute(ic::prefix_own_kernel<D, 2>, max, ic::OwnSmem<D>::BYTES);
+    cudaFuncSetAttribute(ic::prefix_own_kernel<D, 4>, max, ic::OwnSmem<D>::BYTES);
 }
 
 bool attn_cluster_available() {
@@ -830,6 +839,8 @@ int device_setup(int* dev_out, int* sms_out) {
                              ic::PrefixSmem<64>::ALLOC);
         cudaFuncSetAttribute(ic::prefix_attn_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ic::PrefixSmem<128>::ALLOC);
+        set_own_attr<64>();
+        set_own_attr<128>();
         cudaFuncSetAttribute(ic::attn_mass_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ic::AM_SMEM);
         cudaFuncSetAttribute(ic::attn_mass_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,

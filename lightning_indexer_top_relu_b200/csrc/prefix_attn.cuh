@@ -65,7 +65,8 @@ struct PrefixAttnArgs {
     float* part_o;              // [B * Lq * Hq, slots, D]
     float* part_lse;            // [B * Lq * Hq, slots] log2-sum-exp
     int B, Lq, P, S, Hq, Hkv, G;
-    int slots;                  // partials per row; 1: out and lse are written directly
+    int slots;                  // partials per row
+    int to_parts;               // partials are written; else (one per row) out and lse directly
     // prefix units: row tiles (pairs of them when shared) x key splits x Hkv
     // (tps: tiles per split; streams: partials of a unit)
     int n_prefix, shared, p_row_units, p_splits, p_tps, p_streams;
@@ -270,10 +271,11 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
     const int my_steps = (steps + 1 - stream) >> 1;
     // a split unit writes one partial per stream that could have a tile
     const bool writes = row_ok && (shared || stream < (prefix ? a.p_streams : a.o_streams));
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may take SMs as they come free
 
     if (nt == 0) {                                                     // nothing visible here
         if (writes) {
-            if (a.slots > 1) {
+            if (a.to_parts) {
                 a.part_lse[row * a.slots + my_slot] = -INFINITY;
             } else {
                 for (int c = 0; c < D / 8; ++c)
@@ -521,7 +523,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             const float lse2 = l_run == 0.0f ? -INFINITY : m_used + log2f(l_run);
             const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
             if (writes) {
-                if (a.slots > 1) a.part_lse[row * a.slots + my_slot] = lse2;
+                if (a.to_parts) a.part_lse[row * a.slots + my_slot] = lse2;
                 else if (a.lse) a.lse[row] = lse2 * LN2;
             }
             if (my_steps > 0) {
@@ -530,7 +532,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                 // query tiles are free: every S was issued before the P V that
                 // o_full waited for.
                 uint8_t* stage = smem + S::OFF_Q + (warp - 4) * 4096;
-                const long long dst_row = writes ? (a.slots > 1 ? row * a.slots + my_slot : row) : -1;
+                const long long dst_row = writes ? (a.to_parts ? row * a.slots + my_slot : row) : -1;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -550,7 +552,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                         const long long dr = __shfl_sync(0xffffffffu, dst_row, lr);
                         const float4 f = *reinterpret_cast<const float4*>(stage + lr * 128 + (((lane & 7) ^ (lr & 7)) << 4));
                         if (dr >= 0) {
-                            if (a.slots > 1) {
+                            if (a.to_parts) {
                                 reinterpret_cast<float4*>(a.part_o + dr * D + c * 32)[lane & 7] = f;
                             } else {
                                 __nv_bfloat162 p0 = __floats2bfloat162_rn(f.x, f.y), p1 = __floats2bfloat162_rn(f.z, f.w);
