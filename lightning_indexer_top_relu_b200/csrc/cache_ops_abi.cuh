@@ -93,20 +93,21 @@ int check_prefix_sizes(int B, int Lq, int P, int S, int Hq) {
 // Work units of a shared-prefix attention and its partials per row.
 struct PrefixGeom {
     bool shared = false;
-    int p_row_units = 0, p_splits = 0, p_tps = 0, p_streams = 0;
-    int o_row_units = 0, o_splits = 0, o_tps = 0, o_streams = 0;
+    int p_row_units = 0, p_splits = 0, p_tps = 0;
+    int o_row_units = 0, o_splits = 0, o_tps = 0;
     int slots = 0;
     long long n_prefix = 0, n_own = 0;
     int ranks = 0;                 // > 0: the own caches and the merge in a kernel of clusters of so many CTAs
     size_t ws_bytes = 0;
 };
 
-// How finely the keys are split: `s` bounds the steps (one stream's 128 rows x
-// 128 keys, about 0.7 us) of a unit, and the s of the smallest estimated time is
-// taken.  A unit costs its steps and about 6 more to start and end; an own
-// tile counts double (64 KB of K and V for one step); merging a partial row
-// costs the time of writing and reading it.  Units up to the number of SMs run
-// at once, more run in turn, the last half a unit late on average.
+// How finely the keys are split, and whether two row tiles share a CTA: `s`
+// bounds the steps (one stream's 128 rows x 128 keys, about 0.9 us) of a unit,
+// and the s of the smallest estimated time is taken.  A unit costs its steps
+// and 6 to 7.5 more to start and to write its partials (a shared unit writes
+// twice as many); an own tile counts double (64 KB of K and V for one step); a
+// partial row also costs its reading by the merge.  Units up to the number of SMs
+// run at once, more run in turn, the last half a unit late on average.
 PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int sms) {
     PrefixGeom g;
     const int T = ic::PA_KEYS, R = ic::PA_ROWS, G = Hq / Hkv;
@@ -115,50 +116,52 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
     // few rows a sequence: the own caches are not units of this kernel
     const bool merge_kernel = ro <= ic::PO_MAX_ROWS && (long long)B * Hkv <= MAX_GRID_X / 8;
     const bool has_p = P > 0, has_o = !merge_kernel && (S > 0 || P == 0);   // no key at all: the own units write zeros
-    // clusters for about four CTAs an SM, with at least 64 keys a key stream
+    // clusters for one wave of two CTAs an SM, with at least 64 keys a key stream
     // or 64 partial rows a CTA
     auto cluster = [&](long long slots) {
         const long long units = (long long)B * Hkv;
         const int kw = ro <= 16 ? 4 : ro <= 32 ? 2 : 1;
         int r = 1;
-        while (r < 8 && units * r * 2 <= 4LL * sms && (S / (r * 2 * kw) >= 64 || ro * slots >= 128LL * r)) r *= 2;
+        while (r < 8 && units * r * 2 <= 2LL * sms && (S / (r * 2 * kw) >= 64 || ro * slots >= 128LL * r)) r *= 2;
         return r;
     };
     if (merge_kernel && !has_p) {
         g.ranks = cluster(0);
         return g;
     }
-    g.shared = rp > R;
-    const int per_step = g.shared ? 2 : 1;
-    if (has_p) g.p_row_units = (int)((rp + R * per_step - 1) / (R * per_step));
     if (has_o) g.o_row_units = (int)((ro + R - 1) / R);
-    const long long n_pu = (long long)g.p_row_units * Hkv, n_ou = (long long)B * g.o_row_units * Hkv;
-    const double p_work = (double)n_pu * p_nt * per_step, o_work = 2.0 * n_ou * o_nt;
-    const double merge = (double)B * Lq * Hq * d * 1.4e-6;
-    const int s_max = std::max(has_p ? p_nt * per_step : 1, has_o ? o_nt : 1);
+    const long long n_ou = (long long)B * g.o_row_units * Hkv;
+    const double o_work = 2.0 * n_ou * o_nt, row_bytes = (double)B * Lq * Hq * d * 4.0;
     double best = -1.0;
-    for (int s = 1;; s = std::min(s_max, s + std::max(1, s / 8))) {
-        const int p_tps = std::min(std::max(1, s / per_step), std::max(1, p_nt));
-        const int o_tps = std::min(std::max(1, s / 2), o_nt);
-        const int p_sp = has_p ? (p_nt + p_tps - 1) / p_tps : 0, o_sp = has_o ? (o_nt + o_tps - 1) / o_tps : 0;
-        const int p_str = g.shared ? 1 : std::min(2, p_tps), o_str = std::min(2, o_tps);
-        const long long slots = (long long)p_sp * p_str + (long long)o_sp * o_str;
-        const double n = (double)n_pu * p_sp + (double)n_ou * o_sp;
-        const double unit = 6.0 + std::max(has_p ? p_tps * per_step : 0, has_o ? 2 * o_tps : 0);
-        double est = n <= sms ? unit : std::max(unit, (p_work + o_work + 6.0 * n) / sms + 0.5 * unit);
-        if (slots > 1 || merge_kernel) est += merge * slots;
-        if (n < 2147483647.0 && (best < 0.0 || est < best)) {
-            best = est;
-            g.p_tps = p_tps; g.o_tps = o_tps;
-            g.p_splits = p_sp; g.o_splits = o_sp;
-            g.p_streams = has_p ? p_str : 0; g.o_streams = has_o ? o_str : 0;
-            g.slots = (int)slots;
+    for (int shared = 0; shared <= (rp > R ? 1 : 0); ++shared) {
+        const int per_step = shared ? 2 : 1;
+        const int row_units = has_p ? (int)((rp + R * per_step - 1) / (R * per_step)) : 0;
+        const long long n_pu = (long long)row_units * Hkv;
+        const double p_work = (double)n_pu * p_nt * per_step, ends = shared ? 7.5 : 6.0;
+        const int s_max = std::max(has_p ? p_nt * per_step : 1, has_o ? o_nt : 1);
+        for (int s = 1;; s = std::min(s_max, s + std::max(1, s / 8))) {
+            const int p_tps = std::min(std::max(1, s / per_step), std::max(1, p_nt));
+            const int o_tps = std::min(std::max(1, s / 2), o_nt);
+            const int p_sp = has_p ? (p_nt + p_tps - 1) / p_tps : 0, o_sp = has_o ? (o_nt + o_tps - 1) / o_tps : 0;
+            const long long slots = (long long)p_sp + o_sp;
+            const double n = (double)n_pu * p_sp + (double)n_ou * o_sp;
+            const double unit = ends + std::max(has_p ? p_tps * per_step : 0, has_o ? 2 * o_tps : 0);
+            double est = n <= sms ? unit : std::max(unit, (p_work + o_work + ends * n) / sms + 0.5 * unit);
+            if (slots > 1 || merge_kernel) est += row_bytes * slots * 3.0e-7;
+            if (n < 2147483647.0 && (best < 0.0 || est < best)) {
+                best = est;
+                g.shared = shared != 0;
+                g.p_row_units = row_units;
+                g.p_tps = p_tps; g.o_tps = o_tps;
+                g.p_splits = p_sp; g.o_splits = o_sp;
+                g.slots = (int)slots;
+                g.n_prefix = n_pu * p_sp;
+                g.n_own = n_ou * o_sp;
+            }
+            if (s >= s_max) break;
         }
-        if (s >= s_max) break;
     }
     if (merge_kernel) g.ranks = cluster(g.slots);
-    g.n_prefix = n_pu * g.p_splits;
-    g.n_own = n_ou * g.o_splits;
     if (g.slots > 1 || merge_kernel) g.ws_bytes = (size_t)B * Lq * Hq * g.slots * (d + 1) * sizeof(float);
     return g;
 }
@@ -294,9 +297,9 @@ int ic_prefix_attn(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* 
     a.slots = g.slots;
     a.n_prefix = (int)g.n_prefix;
     a.shared = g.shared ? 1 : 0;
-    a.p_row_units = g.p_row_units; a.p_splits = g.p_splits; a.p_tps = g.p_tps; a.p_streams = g.p_streams;
-    a.o_row_units = g.o_row_units; a.o_splits = g.o_splits; a.o_tps = g.o_tps; a.o_streams = g.o_streams;
-    a.o_slot0 = g.p_splits * g.p_streams;
+    a.p_row_units = g.p_row_units; a.p_splits = g.p_splits; a.p_tps = g.p_tps;
+    a.o_row_units = g.o_row_units; a.o_splits = g.o_splits; a.o_tps = g.o_tps;
+    a.o_slot0 = g.p_splits;
     a.scale_log2 = scale_log2_of(scale, d);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)(g.n_prefix + g.n_own);

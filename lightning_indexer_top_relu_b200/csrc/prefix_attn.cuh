@@ -17,10 +17,12 @@
 // One CTA (1 per SM): two streams, each a 128-row query tile (TMEM lanes) with
 // its own score buffers, output accumulator and softmax warpgroup, so one
 // stream's exponentials overlap the other's.
-//   shared units (more than 128 rows over the prefix): the streams are two row
+//   shared units (many rows and tiles over the prefix): the streams are two row
 //     tiles, both of which use every K/V tile;
-//   split units (own caches, or a prefix with at most 128 rows): both streams
-//     hold the same rows and take alternate K/V tiles (two partials).
+//   split units (own caches, or a prefix whose keys are split so far that a
+//     CTA has few tiles): both streams hold the same rows and take alternate
+//     K/V tiles; their results are merged in the CTA, so that half as many
+//     partial rows are written.
 // Step n of a unit belongs to stream n & 1 and the 128-key tile n >> 1 (shared)
 // or n (split).
 //   warp 0      TMA: 128-key tiles of K and V, alternately, into one ring.
@@ -68,10 +70,10 @@ struct PrefixAttnArgs {
     int slots;                  // partials per row
     int to_parts;               // partials are written; else (one per row) out and lse directly
     // prefix units: row tiles (pairs of them when shared) x key splits x Hkv
-    // (tps: tiles per split; streams: partials of a unit)
-    int n_prefix, shared, p_row_units, p_splits, p_tps, p_streams;
+    // (tps: tiles per split)
+    int n_prefix, shared, p_row_units, p_splits, p_tps;
     // own units: B x row tiles x key splits x Hkv; their partials start at slot o_slot0
-    int o_row_units, o_splits, o_tps, o_slot0, o_streams;
+    int o_row_units, o_splits, o_tps, o_slot0;
     float scale_log2;
 };
 
@@ -97,7 +99,8 @@ struct PrefixSmem {
     static constexpr int OFF_BAR = OFF_KV + STAGES * STAGE;
     static constexpr int N_BARS = 2 * STAGES + 10;
     static constexpr int OFF_SLOT = OFF_BAR + N_BARS * 8;
-    static constexpr int BYTES = OFF_SLOT + 16;
+    static constexpr int OFF_LSE = OFF_SLOT + 16;            // both streams' log2-sum-exps
+    static constexpr int BYTES = OFF_LSE + 2 * PA_ROWS * 4;
     static constexpr int ALLOC = BYTES + 1024;               // slack for the 1024-byte alignment
     static_assert(ALLOC <= MAX_DYN_SMEM, "shared memory of one CTA");
 };
@@ -235,7 +238,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         r0 = ru * (a.shared ? 2 * PA_ROWS : PA_ROWS);
         key0 = sp * a.p_tps * PA_KEYS;
         key_end = (int)min((long long)a.P, (long long)key0 + (long long)a.p_tps * PA_KEYS);
-        slot = a.p_streams * sp;
+        slot = sp;
     } else {
         u -= a.n_prefix;
         const int sp = u % a.o_splits;
@@ -252,7 +255,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         const int vis = max(0, own_len - a.Lq + i_last + 1);           // of the last row: the most
         key0 = sp * a.o_tps * PA_KEYS;
         key_end = (int)min((long long)vis, (long long)key0 + (long long)a.o_tps * PA_KEYS);
-        slot = a.o_slot0 + a.o_streams * sp;
+        slot = a.o_slot0 + sp;
     }
     const bool shared = prefix && a.shared;
     const int nt = key_end > key0 ? (key_end - key0 + PA_KEYS - 1) / PA_KEYS : 0;
@@ -267,16 +270,13 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
     const int bi = bi0 + r / a.G;                                      // b * Lq + i
     const long long row = (long long)bi * a.Hq + j * a.G + r % a.G;
     const int vis = !row_ok ? 0 : (prefix ? a.P : max(0, own_len - a.Lq + r / a.G + 1));
-    const int my_slot = slot + (shared ? 0 : stream);
     const int my_steps = (steps + 1 - stream) >> 1;
-    // a split unit writes one partial per stream that could have a tile
-    const bool writes = row_ok && (shared || stream < (prefix ? a.p_streams : a.o_streams));
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may take SMs as they come free
 
     if (nt == 0) {                                                     // nothing visible here
-        if (writes) {
+        if (row_ok && (shared || stream == 0)) {
             if (a.to_parts) {
-                a.part_lse[row * a.slots + my_slot] = -INFINITY;
+                a.part_lse[row * a.slots + slot] = -INFINITY;
             } else {
                 for (int c = 0; c < D / 8; ++c)
                     reinterpret_cast<uint4*>(a.out + row * D)[c] = make_uint4(0, 0, 0, 0);
@@ -519,46 +519,94 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             ok = __all_sync(0xffffffffu, mbar_wait(&o_full[stream], (my_steps - 1) & 1));
             tc_fence_after();
         }
-        if (ok) {                                   // uniform across the warp
-            const float lse2 = l_run == 0.0f ? -INFINITY : m_used + log2f(l_run);
-            const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
-            if (writes) {
-                if (a.to_parts) a.part_lse[row * a.slots + my_slot] = lse2;
-                else if (a.lse) a.lse[row] = lse2 * LN2;
-            }
-            if (my_steps > 0) {
-                // O / l through shared memory, 32 columns of the warp's 32 rows at
-                // a time, so that global writes are whole 128-byte lines.  The
-                // query tiles are free: every S was issued before the P V that
-                // o_full waited for.
-                uint8_t* stage = smem + S::OFF_Q + (warp - 4) * 4096;
-                const long long dst_row = writes ? (a.to_parts ? row * a.slots + my_slot : row) : -1;
+        // ---------------- results: O / l and the log2-sum-exp of each row
+        float lse2 = l_run == 0.0f ? -INFINITY : m_used + log2f(l_run);
+        float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+        // The query tiles are free: every S was issued before the P V that
+        // o_full waited for; in split units once both streams have waited.
+        uint8_t* stage = smem + S::OFF_Q + (warp - 4) * 4096;
+        int c0 = 0, c1 = D / 32;                                       // this warp's 32-column chunks
+        const float* other = nullptr;                                  // the other stream's part of them
+        float w_own = 1.0f, w_other = 0.0f;
+        if (!shared) {
+            // split units: the streams have halves of the keys of the same rows.
+            // Each hands the other half of the columns over through shared
+            // memory (the query tiles' space; the rings stage the writes) and
+            // finishes its own half.
+            float* lses = reinterpret_cast<float*>(smem + S::OFF_LSE);                 // [2][128]
+            float* give = reinterpret_cast<float*>(smem + S::OFF_Q + stream * S::QTILE);   // [128][D / 2]
+            lses[stream * PA_ROWS + tr] = lse2;
+            named_bar(1, 256);                                         // both streams' MMAs are done
+            const int half = D / 64;                                   // chunks a stream finishes
+            if (ok && my_steps > 0) {
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; c < half; ++c) {
                     uint32_t o[32];
-                    __syncwarp();
-                    tmem_ld_32x32b_x32(ob + c * 32, o);
+                    tmem_ld_32x32b_x32(ob + ((stream ^ 1) * half + c) * 32, o);
                     tmem_ld_wait(o);
-                    // a row that saw nothing has P = 0 and is written as 0
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                        *reinterpret_cast<float4*>(give + tr * (D / 2) + (((c * 8 + e) ^ (tr & 7)) << 2)) =
                             make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
                                         __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
-                    __syncwarp();
+                }
+            }
+            named_bar(1, 256);
+            const float l_other = lses[(stream ^ 1) * PA_ROWS + tr], M = fmaxf(lse2, l_other);
+            const float e_own = lse2 == -INFINITY ? 0.0f : ex2_approx(lse2 - M);
+            const float e_other = l_other == -INFINITY ? 0.0f : ex2_approx(l_other - M);
+            const float W = e_own + e_other;
+            w_own = W == 0.0f ? 0.0f : e_own / W;
+            w_other = W == 0.0f ? 0.0f : e_other / W;
+            lse2 = W == 0.0f ? -INFINITY : M + log2f(W);
+            inv *= w_own;
+            other = reinterpret_cast<const float*>(smem + S::OFF_Q + (stream ^ 1) * S::QTILE) + tr * (D / 2);
+            c0 = stream * half;
+            c1 = c0 + half;
+            stage = smem + S::OFF_KV + (warp - 4) * 4096;
+        }
+        if (ok) {                                   // uniform across the warp
+            if (row_ok && (shared || stream == 0)) {
+                if (a.to_parts) a.part_lse[row * a.slots + slot] = lse2;
+                else if (a.lse) a.lse[row] = lse2 * LN2;
+            }
+            // through shared memory, 32 columns of the warp's 32 rows at a time, so
+            // that global writes are whole 128-byte lines
+            const long long dst_row = row_ok ? (a.to_parts ? row * a.slots + slot : row) : -1;
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+                uint32_t o[32];
+                __syncwarp();
+                tmem_ld_32x32b_x32(ob + c * 32, o);
+                tmem_ld_wait(o);
+                // nothing seen (or, in this stream, no tile at all): weight 0, whatever O holds
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float4 f = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                           __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+                    if (inv == 0.0f) f = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (w_other != 0.0f) {
+                        const float4 g = *reinterpret_cast<const float4*>(other + ((((c - c0) * 8 + e) ^ (tr & 7)) << 2));
+                        f.x = fmaf(w_other, g.x, f.x);
+                        f.y = fmaf(w_other, g.y, f.y);
+                        f.z = fmaf(w_other, g.z, f.z);
+                        f.w = fmaf(w_other, g.w, f.w);
+                    }
+                    *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = f;
+                }
+                __syncwarp();
 #pragma unroll 2
-                    for (int x = 0; x < 8; ++x) {
-                        const int lr = x * 4 + (lane >> 3);
-                        const long long dr = __shfl_sync(0xffffffffu, dst_row, lr);
-                        const float4 f = *reinterpret_cast<const float4*>(stage + lr * 128 + (((lane & 7) ^ (lr & 7)) << 4));
-                        if (dr >= 0) {
-                            if (a.to_parts) {
-                                reinterpret_cast<float4*>(a.part_o + dr * D + c * 32)[lane & 7] = f;
-                            } else {
-                                __nv_bfloat162 p0 = __floats2bfloat162_rn(f.x, f.y), p1 = __floats2bfloat162_rn(f.z, f.w);
-                                reinterpret_cast<uint2*>(a.out + dr * D + c * 32)[lane & 7] =
-                                    make_uint2(*reinterpret_cast<uint32_t*>(&p0), *reinterpret_cast<uint32_t*>(&p1));
-                            }
+                for (int x = 0; x < 8; ++x) {
+                    const int lr = x * 4 + (lane >> 3);
+                    const long long dr = __shfl_sync(0xffffffffu, dst_row, lr);
+                    const float4 f = *reinterpret_cast<const float4*>(stage + lr * 128 + (((lane & 7) ^ (lr & 7)) << 4));
+                    if (dr >= 0) {
+                        if (a.to_parts) {
+                            reinterpret_cast<float4*>(a.part_o + dr * D + c * 32)[lane & 7] = f;
+                        } else {
+                            __nv_bfloat162 p0 = __floats2bfloat162_rn(f.x, f.y), p1 = __floats2bfloat162_rn(f.z, f.w);
+                            reinterpret_cast<uint2*>(a.out + dr * D + c * 32)[lane & 7] =
+                                make_uint2(*reinterpret_cast<uint32_t*>(&p0), *reinterpret_cast<uint32_t*>(&p1));
                         }
                     }
                 }

@@ -9,11 +9,12 @@
 // as tcgen05 units).
 //
 // One thread-block cluster of `ranks` CTAs per (sequence, K/V head); a CTA has
-// four warps, MT row tiles x 4 / MT key streams.  Blocks of 16 keys go to the
-// cluster's key streams in turn; each warp copies its blocks through a
-// cp.async ring of its own (keys past the sequence's length are
-// filled with zeros) and runs an online softmax, its exponent base moving only
-// when a block's maximum passes it by more than 2^8.  The partials meet in
+// four warps, MT row tiles x 4 / MT key streams.  Sets of MT blocks of 16 keys go
+// to the cluster's key streams in turn; each of a stream's MT warps copies one
+// block of a set through a cp.async ring (keys past the sequence's length are
+// filled with zeros) and works on all of them for its row tile, with an online
+// softmax whose exponent base moves only when a block's maximum passes it by
+// more than 2^8.  The partials meet in
 // shared memory and, over the cluster, in distributed shared memory; rank r
 // finishes rows r, r + ranks, ...: it waits for the prefix kernel
 // (programmatic dependent launch: up to there the two overlap) and adds the
@@ -77,17 +78,18 @@ prefix_own_kernel(const PrefixOwnArgs a) {
     const int n = a.S > 0 ? seq_len(a.lens, b, a.S) : 0;
     const int R = a.Lq * a.G;
     auto row_of = [&](int r) { return ((long long)b * a.Lq + r / a.G) * a.Hq + j * a.G + r % a.G; };
-    const uint32_t ring = smem_u32(po_smem) + warp * S::WARP;
+    // stage st of warp w of this key stream (its block of a set)
+    auto stage = [&](int w, int st) { return smem_u32(po_smem) + (kw * MT + w) * S::WARP + st * S::STAGE; };
 
-    // blocks x = sid, sid + streams, ...
-    const int nblk = (n + PO_BLOCK - 1) / PO_BLOCK, streams = a.ranks * KW, sid = rank * KW + kw;
-    const int niter = nblk > sid ? (nblk - sid + streams - 1) / streams : 0;
+    // sets x = sid, sid + streams, ... of MT blocks
+    const int nset = (n + MT * PO_BLOCK - 1) / (MT * PO_BLOCK), streams = a.ranks * KW, sid = rank * KW + kw;
+    const int niter = nset > sid ? (nset - sid + streams - 1) / streams : 0;
     const long long krow = (long long)a.Hkv * D;                     // elements from key to key
     const __nv_bfloat16* kb = a.k + ((long long)b * a.S * a.Hkv + j) * D + (lane % CPR) * 8;
     const __nv_bfloat16* vb = a.v + ((long long)b * a.S * a.Hkv + j) * D + (lane % CPR) * 8;
     auto issue = [&](int it, int st) {
-        const int key0 = (sid + it * streams) * PO_BLOCK;
-        const uint32_t kdst = ring + st * S::STAGE, vdst = kdst + S::BLK;
+        const int key0 = ((sid + it * streams) * MT + mt) * PO_BLOCK;
+        const uint32_t kdst = stage(mt, st), vdst = kdst + S::BLK;
 #pragma unroll
         for (int x = 0; x < PO_BLOCK / RPI; ++x) {
             const int r = x * RPI + lane / CPR;
@@ -96,6 +98,11 @@ prefix_own_kernel(const PrefixOwnArgs a) {
             cp_async16(kdst + swz<D>(r, lane % CPR), kb + off, ok);
             cp_async16(vdst + swz<D>(r, lane % CPR), vb + off, ok);
         }
+    };
+    // the warps of a key stream (they all have niter sets)
+    auto stream_sync = [&]() {
+        if (MT == 1) __syncwarp();
+        else named_bar(1 + kw, 32 * MT);
     };
 #pragma unroll
     for (int st = 0; st < PO_STAGES - 1; ++st) {
@@ -127,13 +134,15 @@ prefix_own_kernel(const PrefixOwnArgs a) {
     for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.0f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
     for (int it = 0; it < niter; ++it) {
+        cp_async_wait<PO_STAGES - 2>();
+        stream_sync();     // set `it` is there, and every warp is done with set it - 1, whose stage is refilled next
         const int nx = it + PO_STAGES - 1;
         if (nx < niter) issue(nx, nx % PO_STAGES);
         cp_async_commit();
-        cp_async_wait<PO_STAGES - 1>();
-        __syncwarp();
-        const int key0 = (sid + it * streams) * PO_BLOCK;
-        const uint32_t kbase = ring + (it % PO_STAGES) * S::STAGE, vbase = kbase + S::BLK;
+#pragma unroll 1
+        for (int blk = 0; blk < MT; ++blk) {
+        const int key0 = ((sid + it * streams) * MT + blk) * PO_BLOCK;
+        const uint32_t kbase = stage(blk, it % PO_STAGES), vbase = kbase + S::BLK;
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -193,7 +202,7 @@ prefix_own_kernel(const PrefixOwnArgs a) {
             mma_bf16(o[2 * dn], pa, b0, b1);
             mma_bf16(o[2 * dn + 1], pa, b2, b3);
         }
-        __syncwarp();      // every lane is done with this stage before it is refilled
+        }
     }
     cp_async_wait<0>();
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
