@@ -55,12 +55,12 @@ struct OwnSmem {
     static constexpr int MROW = D + 8;                               // padded merge rows
     // merge buffers reuse the rings: [4 warps][16][MROW] f32 (the first key
     // stream's rows end up with the CTA's result), [4][16][2] base and sum,
-    // [64][4] weights, [64] log2-sum-exp, [4][D] + [4] scratch of the last merge
+    // [64][4] weights, [64] log2-sum-exp, [4][D] + [4][2] scratch of the last merge
     static constexpr int MERGE_ML = 4 * 16 * MROW * 4;
     static constexpr int WGT = MERGE_ML + 4 * 16 * 2 * 4;
     static constexpr int LSE = WGT + PO_MAX_ROWS * 4 * 4;
     static constexpr int SCR = LSE + PO_MAX_ROWS * 4;
-    static constexpr int MERGE = SCR + 4 * D * 4 + 16;
+    static constexpr int MERGE = SCR + 4 * D * 4 + 32;
     static constexpr int BYTES = MERGE > 4 * WARP ? MERGE : 4 * WARP;
 };
 
@@ -268,66 +268,32 @@ prefix_own_kernel(const PrefixOwnArgs a) {
 
     // ---------------- the row over all ranks and prefix partials
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // Loads are unconditional (past the end: the last item again) and come
-    // eight at a time: loads behind branches ran one after the other.
+    // A row's items are the ranks' results and its prefix partials, taken eight
+    // at a time with an online softmax over their log2-sum-exps.  Loads are
+    // unconditional (past the end: the last item again): loads behind branches
+    // ran one after the other.  Four warps share a single row, two share each
+    // of two or three, a warp takes one of more.
     constexpr int E = D / 32, UN = 8;                                // columns a lane, items at once (ranks <= 8)
-    auto own_lse = [&](int r) {                                      // lane x: rank x's
-        return a.ranks > 1 ? __uint_as_float(ld_dsmem_u32(smem_u32(row_lse + r), (uint32_t)min(lane, a.ranks - 1)))
-                           : row_lse[r];
-    };
-    // largest log2-sum-exp of a row's items
-    auto row_max = [&](int r, const float* pl) {
-        float M = own_lse(r);
-        for (int x = lane; x < a.slots; x += 32) M = fmaxf(M, pl[x]);
+    const int my_rows = (R - rank + a.ranks - 1) / a.ranks;          // rows rank, rank + ranks, ...
+    const int gw = my_rows >= 4 ? 1 : my_rows >= 2 ? 2 : 4, sub = warp % gw;
+    float M, W, acc[E];
+    auto add = [&](const float (&l)[UN], const float (&v)[UN][E]) {
+        float bm = M;
 #pragma unroll
-        for (int h = 16; h >= 1; h >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, h));
-        return M;
-    };
-    // adds the weighted values of a row's own ranks (`own`) and of the prefix
-    // partials 8 first, 8 first + 1 .. 8 first + 7, 8 (first + step), ... to acc and their weights to W
-    auto add_items = [&](int r, const float* pl, const float* po, float M, bool own, int first, int step, float& W,
-                         float (&acc)[E]) {
-        if (own) {
-            const float l = own_lse(r);
-            const float w = lane >= a.ranks || l == -INFINITY ? 0.0f : sa_ex2(l - M);
-            float v[UN][E];
-            const float* src = mo + r * S::MROW + lane * E;
-            if (a.ranks > 1) {
+        for (int u = 0; u < UN; ++u) bm = fmaxf(bm, l[u]);
+        const float al = M == -INFINITY ? 0.0f : sa_ex2(M - bm);     // nothing was added while M was -inf
+        if (M != -INFINITY) W *= al;                                 // (or sums that are not numbers, which stay)
 #pragma unroll
-                for (int x = 0; x < UN; ++x) ld_dsmem(smem_u32(src), (uint32_t)min(x, a.ranks - 1), v[x]);
-            } else {
+        for (int e = 0; e < E; ++e) acc[e] *= al;
 #pragma unroll
-                for (int x = 0; x < UN; ++x)
+        for (int u = 0; u < UN; ++u) {
+            const float w = l[u] == -INFINITY ? 0.0f : sa_ex2(l[u] - bm);
+            W += w;
+            // an empty partial's values are not written: they may be anything
 #pragma unroll
-                    for (int e = 0; e < E; ++e) v[x][e] = x == 0 ? src[e] : 0.0f;
-            }
-#pragma unroll
-            for (int x = 0; x < UN; ++x) {
-                const float wx = __shfl_sync(0xffffffffu, w, x);
-                W += wx;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(wx, v[x][e], acc[e]);
-            }
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(w, w == 0.0f ? 0.0f : v[u][e], acc[e]);
         }
-        for (int s0 = first * UN; s0 < a.slots; s0 += step * UN) {
-            const float l = pl[min(s0 + (lane & (UN - 1)), a.slots - 1)];
-            const float w = s0 + (lane & (UN - 1)) >= a.slots || l == -INFINITY ? 0.0f : sa_ex2(l - M);
-            float v[UN][E];
-#pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                const float* src = po + (long long)min(s0 + u, a.slots - 1) * D + lane * E;
-                if (E == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src);
-                else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src);
-            }
-#pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                const float wu = __shfl_sync(0xffffffffu, w, u);
-                W += wu;
-                // an empty partial's values are not written: they may be anything
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(wu, wu == 0.0f ? 0.0f : v[u][e], acc[e]);
-            }
-        }
+        M = bm;
     };
     auto finish = [&](long long row, float M, float W, const float (&acc)[E]) {
         const float inv = W == 0.0f ? 0.0f : 1.0f / W;
@@ -339,38 +305,80 @@ prefix_own_kernel(const PrefixOwnArgs a) {
         else dst[0] = w[0];
         if (a.lse && lane == 0) a.lse[row] = W == 0.0f ? -INFINITY : (M == -INFINITY ? W : M + log2f(W)) * LN2;
     };
-    if (a.slots <= 16) {
-        // few partials: a warp a row
-        for (int r = rank + warp * a.ranks; r < R; r += 4 * a.ranks) {
-            const long long row = row_of(r);
-            const float* pl = a.part_lse + row * a.slots;
-            float acc[E] = {}, W = 0.0f;
-            const float M = row_max(r, pl);
-            add_items(r, pl, a.part_o + row * a.slots * D, M, true, 0, 1, W, acc);
-            finish(row, M, W, acc);
+    for (int r0 = rank; r0 < R; r0 += a.ranks * (4 / gw)) {
+        const int r = r0 + warp / gw * a.ranks;
+        const bool on = r < R;                                       // uniform over the warp
+        const long long row = row_of(on ? r : rank);
+        M = -INFINITY;
+        W = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+        if (on && sub == 0) {
+            float l[UN], v[UN][E];
+            const float* src = mo + r * S::MROW + lane * E;
+            if (a.ranks > 1) {
+#pragma unroll
+                for (int x = 0; x < UN; ++x) {
+                    const uint32_t from = (uint32_t)min(x, a.ranks - 1);
+                    l[x] = __uint_as_float(ld_dsmem_u32(smem_u32(row_lse + r), from));
+                    ld_dsmem(smem_u32(src), from, v[x]);
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < UN; ++x) {
+                    l[x] = row_lse[r];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[x][e] = src[e];
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < UN; ++x)
+                if (x >= a.ranks) l[x] = -INFINITY;
+            add(l, v);
         }
-    } else {
-        // many: the four warps share a row's partials
-        for (int r = rank; r < R; r += a.ranks) {
-            const long long row = row_of(r);
+        if (on) {
             const float* pl = a.part_lse + row * a.slots;
-            float acc[E] = {}, W = 0.0f;
-            const float M = row_max(r, pl);
-            add_items(r, pl, a.part_o + row * a.slots * D, M, warp == 0, warp, 4, W, acc);
+            const float* po = a.part_o + row * a.slots * D + lane * E;
+            for (int s0 = sub * UN; s0 < a.slots; s0 += gw * UN) {
+                float l[UN], v[UN][E];
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    const int x = min(s0 + u, a.slots - 1);
+                    l[u] = pl[x];
+                    const float* src = po + (long long)x * D;
+                    if (E == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src);
+                    else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src);
+                }
+#pragma unroll
+                for (int u = 0; u < UN; ++u)
+                    if (s0 + u >= a.slots) l[u] = -INFINITY;
+                add(l, v);
+            }
+        }
+        if (gw > 1) {                                                // uniform over the CTA
+            // the group's warps meet in shared memory; its first one finishes
+            __syncthreads();
 #pragma unroll
             for (int e = 0; e < E; ++e) scr[warp * D + lane * E + e] = acc[e];
-            if (lane == 0) scr[4 * D + warp] = W;
+            if (lane == 0) *reinterpret_cast<float2*>(scr + 4 * D + 2 * warp) = make_float2(M, W);
             __syncthreads();
-            if (warp == 0) {
+            if (sub == 0) {
+                float l[UN], v[UN][E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int c = lane * E + e;
-                    acc[e] = (scr[c] + scr[D + c]) + (scr[2 * D + c] + scr[3 * D + c]);
+                for (int u = 0; u < UN; ++u) {
+                    const int w = warp + min(u, gw - 1);
+                    const float2 mw = *reinterpret_cast<const float2*>(scr + 4 * D + 2 * w);
+                    // as one item: its values over W, its log2-sum-exp (or what is not a number)
+                    const bool more = u > 0 && u < gw;
+                    l[u] = !more || mw.y == 0.0f ? -INFINITY : mw.x == -INFINITY ? mw.y : mw.x + log2f(mw.y);
+                    const float inv = more && mw.y != 0.0f ? 1.0f / mw.y : 0.0f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[u][e] = scr[w * D + lane * E + e] * inv;
                 }
-                finish(row, M, (scr[4 * D] + scr[4 * D + 1]) + (scr[4 * D + 2] + scr[4 * D + 3]), acc);
+                add(l, v);
             }
-            __syncthreads();
         }
+        if (on && sub == 0) finish(row, M, W, acc);
     }
     if (a.ranks > 1) cluster_sync();       // no CTA leaves while another may read its shared memory
 }
