@@ -97,7 +97,7 @@ struct PrefixGeom {
     int o_row_units = 0, o_splits = 0, o_tps = 0;
     int slots = 0;
     long long n_prefix = 0, n_own = 0;
-    int ranks = 0;                 // > 0: the own caches and the merge in a kernel of clusters of so many CTAs
+    bool own_kernel = false;       // the own caches in their own kernel (o_splits CTAs a sequence and K/V head)
     size_t ws_bytes = 0;
 };
 
@@ -113,22 +113,22 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
     const int T = ic::PA_KEYS, R = ic::PA_ROWS, G = Hq / Hkv;
     const long long rp = (long long)B * Lq * G, ro = (long long)Lq * G;
     const int p_nt = (P + T - 1) / T, o_nt = std::max(1, (S + T - 1) / T);
-    // few rows a sequence: the own caches are not units of this kernel
-    const bool merge_kernel = ro <= ic::PO_MAX_ROWS && (long long)B * Hkv <= MAX_GRID_X / 8;
-    const bool has_p = P > 0, has_o = !merge_kernel && (S > 0 || P == 0);   // no key at all: the own units write zeros
-    // clusters for one wave of two CTAs an SM, with at least 64 keys a key stream
-    // or 64 partial rows a CTA
-    auto cluster = [&](long long slots) {
+    // few rows a sequence: the own caches have a kernel of their own, one wave
+    // of two CTAs an SM with at least 64 keys a key stream
+    const bool has_p = P > 0;
+    g.own_kernel = ro <= ic::PO_MAX_ROWS && S > 0 && (long long)B * Hkv <= MAX_GRID_X / 64;
+    if (g.own_kernel) {
         const long long units = (long long)B * Hkv;
         const int kw = ro <= 16 ? 4 : ro <= 32 ? 2 : 1;
-        int r = 1;
-        while (r < 8 && units * r * 2 <= 2LL * sms && (S / (r * 2 * kw) >= 64 || ro * slots >= 128LL * r)) r *= 2;
-        return r;
-    };
-    if (merge_kernel && !has_p) {
-        g.ranks = cluster(0);
-        return g;
+        g.o_splits = (int)std::max(1LL, std::min<long long>({64, 2LL * sms / units, S / (64 * kw)}));
+        if (!has_p) {
+            g.slots = g.o_splits;
+            if (g.slots > 1) g.ws_bytes = (size_t)B * Lq * Hq * g.slots * (d + 1) * sizeof(float);
+            return g;
+        }
     }
+    const bool has_o = !g.own_kernel && (S > 0 || P == 0);   // no key at all: the own units write zeros
+    const int own_slots = g.o_splits;
     if (has_o) g.o_row_units = (int)((ro + R - 1) / R);
     const long long n_ou = (long long)B * g.o_row_units * Hkv;
     const double o_work = 2.0 * n_ou * o_nt, row_bytes = (double)B * Lq * Hq * d * 4.0;
@@ -143,17 +143,18 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
             const int p_tps = std::min(std::max(1, s / per_step), std::max(1, p_nt));
             const int o_tps = std::min(std::max(1, s / 2), o_nt);
             const int p_sp = has_p ? (p_nt + p_tps - 1) / p_tps : 0, o_sp = has_o ? (o_nt + o_tps - 1) / o_tps : 0;
-            const long long slots = (long long)p_sp + o_sp;
+            const long long slots = (long long)p_sp + o_sp + own_slots;
             const double n = (double)n_pu * p_sp + (double)n_ou * o_sp;
             const double unit = ends + std::max(has_p ? p_tps * per_step : 0, has_o ? 2 * o_tps : 0);
             double est = n <= sms ? unit : std::max(unit, (p_work + o_work + ends * n) / sms + 0.5 * unit);
-            if (slots > 1 || merge_kernel) est += row_bytes * slots * 3.0e-7;
+            if (slots > 1) est += row_bytes * slots * 3.0e-7;
             if (n < 2147483647.0 && (best < 0.0 || est < best)) {
                 best = est;
                 g.shared = shared != 0;
                 g.p_row_units = row_units;
                 g.p_tps = p_tps; g.o_tps = o_tps;
-                g.p_splits = p_sp; g.o_splits = o_sp;
+                g.p_splits = p_sp;
+                if (has_o) g.o_splits = o_sp;
                 g.slots = (int)slots;
                 g.n_prefix = n_pu * p_sp;
                 g.n_own = n_ou * o_sp;
@@ -161,8 +162,7 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
             if (s >= s_max) break;
         }
     }
-    if (merge_kernel) g.ranks = cluster(g.slots);
-    if (g.slots > 1 || merge_kernel) g.ws_bytes = (size_t)B * Lq * Hq * g.slots * (d + 1) * sizeof(float);
+    if (g.slots > 1) g.ws_bytes = (size_t)B * Lq * Hq * g.slots * (d + 1) * sizeof(float);
     return g;
 }
 
@@ -187,8 +187,24 @@ int make_tmap(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, 
     return IC_OK;
 }
 
-// The second kernel: own caches and merge.  After a prefix kernel it is launched as its
-// programmatic dependent.
+// Launches `kernel`; with `dependent` as the programmatic dependent of the
+// kernel before it on the stream, whose results it waits for itself.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, bool dependent,
+                             cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 int launch_prefix_own(const PrefixGeom& g, const ic::PrefixAttnArgs& p, const uint16_t* k, const uint16_t* v, int d,
                       bool dependent, cudaStream_t st) {
     ic::PrefixOwnArgs a{};
@@ -200,35 +216,26 @@ int launch_prefix_own(const PrefixGeom& g, const ic::PrefixAttnArgs& p, const ui
     a.lse = p.lse;
     a.part_o = p.part_o;
     a.part_lse = p.part_lse;
-    a.slots = dependent ? g.slots : 0;
+    a.slots = p.slots;
+    a.slot0 = p.o_slot0;
+    a.to_parts = p.to_parts;
     a.B = p.B; a.Lq = p.Lq; a.S = p.S; a.Hq = p.Hq; a.Hkv = p.Hkv; a.G = p.G;
-    a.ranks = g.ranks;
+    a.splits = g.o_splits;
     a.scale_log2 = p.scale_log2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(g.ranks * p.B * p.Hkv));
-    cfg.blockDim = dim3(ic::PO_THREADS);
-    cfg.dynamicSmemBytes = d == 64 ? ic::OwnSmem<64>::BYTES : ic::OwnSmem<128>::BYTES;
-    cfg.stream = st;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)g.ranks;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = dependent ? 2 : 1;
+    const unsigned grid = (unsigned)((long long)p.B * p.Hkv * g.o_splits);
     const int rows = p.Lq * p.G;
-    cudaError_t e;
+    auto run = [&](void (*kernel)(const ic::PrefixOwnArgs), size_t smem) {
+        return launched(launch_dependent(kernel, grid, ic::PO_THREADS, smem, dependent, st, a), "prefix_attn own launch");
+    };
     if (d == 64)
-        e = rows <= 16   ? cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<64, 1>, a)
-            : rows <= 32 ? cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<64, 2>, a)
-                         : cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<64, 4>, a);
-    else
-        e = rows <= 16   ? cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<128, 1>, a)
-            : rows <= 32 ? cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<128, 2>, a)
-                         : cudaLaunchKernelEx(&cfg, ic::prefix_own_kernel<128, 4>, a);
-    return launched(e, "prefix_attn own launch");
+        return run(rows <= 16   ? ic::prefix_own_kernel<64, 1>
+                   : rows <= 32 ? ic::prefix_own_kernel<64, 2>
+                                : ic::prefix_own_kernel<64, 4>,
+                   ic::OwnSmem<64>::BYTES);
+    return run(rows <= 16   ? ic::prefix_own_kernel<128, 1>
+               : rows <= 32 ? ic::prefix_own_kernel<128, 2>
+                            : ic::prefix_own_kernel<128, 4>,
+               ic::OwnSmem<128>::BYTES);
 }
 
 }  // namespace
@@ -278,7 +285,7 @@ int ic_prefix_attn(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* 
         if ((rc = make_tmap(&tkp, k_prefix, 3, dims, strides, box))) return rc;
         if ((rc = make_tmap(&tvp, v_prefix, 3, dims, strides, box))) return rc;
     }
-    if (S > 0) {
+    if (S > 0 && !g.own_kernel) {
         const uint64_t dims[4] = {(uint64_t)d, (uint64_t)Hkv, (uint64_t)S, (uint64_t)B};
         const uint64_t strides[3] = {(uint64_t)d * 2, hd * 2, hd * 2 * S};
         const uint32_t box[4] = {64, 1, ic::PA_KEYS, 1};
@@ -303,26 +310,21 @@ int ic_prefix_attn(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* 
     a.scale_log2 = scale_log2_of(scale, d);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)(g.n_prefix + g.n_own);
-    a.to_parts = g.ranks > 0 || g.slots > 1 ? 1 : 0;
-    if (grid == 0) {
-        // no prefix
-    } else if (d == 64)
-        ic::prefix_attn_kernel<64><<<grid, ic::PA_THREADS, ic::PrefixSmem<64>::ALLOC, st>>>(tkp, tvp, tk, tv, a);
-    else
-        ic::prefix_attn_kernel<128><<<grid, ic::PA_THREADS, ic::PrefixSmem<128>::ALLOC, st>>>(tkp, tvp, tk, tv, a);
-    if (grid > 0 && launched(cudaGetLastError(), "prefix_attn launch")) return IC_ERR_CUDA;
-    if (g.ranks > 0) return launch_prefix_own(g, a, k, v, d, grid > 0, st);
+    a.to_parts = g.slots > 1 ? 1 : 0;
+    if (grid > 0) {
+        if (d == 64)
+            ic::prefix_attn_kernel<64><<<grid, ic::PA_THREADS, ic::PrefixSmem<64>::ALLOC, st>>>(tkp, tvp, tk, tv, a);
+        else
+            ic::prefix_attn_kernel<128><<<grid, ic::PA_THREADS, ic::PrefixSmem<128>::ALLOC, st>>>(tkp, tvp, tk, tv, a);
+        if (launched(cudaGetLastError(), "prefix_attn launch")) return IC_ERR_CUDA;
+    }
+    if (g.own_kernel && (rc = launch_prefix_own(g, a, k, v, d, grid > 0, st))) return rc;
     if (g.slots == 1) return IC_OK;
     const bool wide = g.slots > 8;
     const unsigned cg = (unsigned)(wide ? rows : (rows + 3) / 4);
-    if (d == 64) {
-        if (wide) ic::prefix_combine_kernel<64, true><<<cg, 128, 0, st>>>(a, rows);
-        else ic::prefix_combine_kernel<64, false><<<cg, 128, 0, st>>>(a, rows);
-    } else {
-        if (wide) ic::prefix_combine_kernel<128, true><<<cg, 128, 0, st>>>(a, rows);
-        else ic::prefix_combine_kernel<128, false><<<cg, 128, 0, st>>>(a, rows);
-    }
-    return launched(cudaGetLastError(), "prefix_attn combine launch");
+    auto* combine = d == 64 ? (wide ? ic::prefix_combine_kernel<64, true> : ic::prefix_combine_kernel<64, false>)
+                            : (wide ? ic::prefix_combine_kernel<128, true> : ic::prefix_combine_kernel<128, false>);
+    return launched(launch_dependent(combine, cg, 128, 0, true, st, a, rows), "prefix_attn combine launch");
 }
 
 size_t ic_attn_mass_workspace_bytes(int B, int Lq, int Lk, int Hq, int Hkv, int d) {

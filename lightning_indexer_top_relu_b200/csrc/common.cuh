@@ -320,18 +320,6 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t local_addr, uint32_t r
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_addr), "r"(rank));
     return remote;
 }
-__device__ __forceinline__ void ld_dsmem(uint32_t local_addr, uint32_t rank, float (&v)[4]) {
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-                 : "r"(cluster_addr(local_addr, rank))
-                 : "memory");
-}
-__device__ __forceinline__ void ld_dsmem(uint32_t local_addr, uint32_t rank, float (&v)[2]) {
-    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
-                 : "=f"(v[0]), "=f"(v[1])
-                 : "r"(cluster_addr(local_addr, rank))
-                 : "memory");
-}
 __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t local_addr, uint32_t rank) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(local_addr, rank)) : "memory");

@@ -630,6 +630,7 @@ prefix_combine_kernel(const PrefixAttnArgs a, long long n_rows) {
     constexpr int E = D / 32;                                   // output columns a lane
     __shared__ float so[4][D], sw[4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");          // launched as the attention's dependent
     const long long row = WIDE ? (long long)blockIdx.x : (long long)blockIdx.x * 4 + warp;
     if (row >= n_rows) return;                                  // WIDE: every row exists
     const float* pl = a.part_lse + row * a.slots;
@@ -639,26 +640,24 @@ prefix_combine_kernel(const PrefixAttnArgs a, long long n_rows) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float W = 0.0f, acc[E] = {};
-    constexpr int STEP = WIDE ? 4 : 1, UN = 4;
+    constexpr int STEP = WIDE ? 4 : 1, UN = 8;
     for (int s0 = WIDE ? warp : 0; s0 < a.slots; s0 += STEP * UN) {
-        float v[UN][E], w[UN];
+        float v[UN][E], l[UN];
+        // unconditional loads (past the end: the last partial again), all under way
+        // at once; an empty partial's O is not written and may be anything
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
-            const int s = s0 + u * STEP;
-            const float l = s < a.slots ? pl[s] : -INFINITY;
-            w[u] = l == -INFINITY ? 0.0f : exp2f(l - M);
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[u][e] = 0.0f;
-            if (l != -INFINITY) {                               // an empty partial's O is not written
-                if (E == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(po + (long long)s * D);
-                else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(po + (long long)s * D);
-            }
+            const int s = min(s0 + u * STEP, a.slots - 1);
+            l[u] = pl[s];
+            if (E == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(po + (long long)s * D);
+            else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(po + (long long)s * D);
         }
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
-            W += w[u];
+            const float w = l[u] == -INFINITY || s0 + u * STEP >= a.slots ? 0.0f : exp2f(l[u] - M);
+            W += w;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(w[u], v[u][e], acc[e]);
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(w, w == 0.0f ? 0.0f : v[u][e], acc[e]);
         }
     }
     if (WIDE) {

@@ -1,24 +1,21 @@
-// Second kernel of the shared-prefix attention when a sequence has few query
+// The own caches of a shared-prefix attention when a sequence has few query
 // rows (decode, drafted tokens): the attention of each sequence's rows over its
-// own cache, and the merge with the rows' partial results over the prefix.
+// own cache, as partial results for the merge.
 //
 // The own caches are read once and have at most 64 rows to feed, so this part
-// is bound by memory bandwidth; tiles of 16 rows on m16n8k16 keep four
-// times the CTAs of the tcgen05 kernel on an SM, whose 128-row tiles would be
-// mostly empty here (32 sequences behind a 32K prefix: 30 us with the own caches
-// as tcgen05 units).
+// is bound by memory bandwidth; tiles of 16 rows on m16n8k16 keep two CTAs
+// on an SM, while the tcgen05 kernel's 128-row tiles would be mostly empty here
+// (256 sequences of up to 1K behind a 64K prefix: 188 us with the own caches as
+// tcgen05 units).  It is a programmatic dependent of the prefix kernel and needs
+// nothing of it, so its CTAs run on the SMs that the prefix units leave idle.
 //
-// One thread-block cluster of `ranks` CTAs per (sequence, K/V head); a CTA has
-// four warps, MT row tiles x 4 / MT key streams.  Sets of MT blocks of 16 keys go
-// to the cluster's key streams in turn; each of a stream's MT warps copies one
-// block of a set through a cp.async ring (keys past the sequence's length are
-// filled with zeros) and works on all of them for its row tile, with an online
-// softmax whose exponent base moves only when a block's maximum passes it by
-// more than 2^8.  The partials meet in
-// shared memory and, over the cluster, in distributed shared memory; rank r
-// finishes rows r, r + ranks, ...: it waits for the prefix kernel
-// (programmatic dependent launch: up to there the two overlap) and adds the
-// row's prefix partials.
+// A CTA has one (sequence, K/V head) and one split of its keys: four warps, MT
+// row tiles x 4 / MT key streams.  Sets of MT blocks of 16 keys go to the
+// splits' key streams in turn; each of a stream's MT warps copies one block of a
+// set through a cp.async ring (keys past the sequence's length are filled with
+// zeros) and works on all of them for its row tile, with an online softmax
+// whose exponent base moves only when a block's maximum passes it by more
+// than 2^8.  The streams merge in shared memory.
 #pragma once
 
 #include "common.cuh"
@@ -39,11 +36,12 @@ struct PrefixOwnArgs {
     const int32_t* lens;        // [B] or null (S)
     __nv_bfloat16* out;         // [B, Lq, Hq, D]
     float* lse;                 // [B, Lq, Hq] or null
-    const float* part_o;        // [B * Lq * Hq, slots, D] prefix partials
-    const float* part_lse;      // [B * Lq * Hq, slots] log2-sum-exp
-    int slots;                  // prefix partials per row (0: no prefix)
+    float* part_o;              // [B * Lq * Hq, slots, D]
+    float* part_lse;            // [B * Lq * Hq, slots] log2-sum-exp
+    int slots, slot0;           // partials per row, the first of this kernel's
+    int to_parts;               // partials are written; else (one per row) out and lse directly
     int B, Lq, S, Hq, Hkv, G;
-    int ranks;                  // CTAs per cluster
+    int splits;                 // CTAs that share a sequence's keys
     float scale_log2;
 };
 
@@ -53,14 +51,12 @@ struct OwnSmem {
     static constexpr int STAGE = 2 * BLK;                            // K then V
     static constexpr int WARP = PO_STAGES * STAGE;
     static constexpr int MROW = D + 8;                               // padded merge rows
-    // merge buffers reuse the rings: [4 warps][16][MROW] f32 (the first key
-    // stream's rows end up with the CTA's result), [4][16][2] base and sum,
-    // [64][4] weights, [64] log2-sum-exp, [4][D] + [4][2] scratch of the last merge
+    // merge buffers reuse the rings: [4 warps][16][MROW] f32, [4][16][2] base
+    // and sum, [64][4] weights, [64] log2-sum-exp
     static constexpr int MERGE_ML = 4 * 16 * MROW * 4;
     static constexpr int WGT = MERGE_ML + 4 * 16 * 2 * 4;
     static constexpr int LSE = WGT + PO_MAX_ROWS * 4 * 4;
-    static constexpr int SCR = LSE + PO_MAX_ROWS * 4;
-    static constexpr int MERGE = SCR + 4 * D * 4 + 32;
+    static constexpr int MERGE = LSE + PO_MAX_ROWS * 4;
     static constexpr int BYTES = MERGE > 4 * WARP ? MERGE : 4 * WARP;
 };
 
@@ -73,16 +69,17 @@ prefix_own_kernel(const PrefixOwnArgs a) {
     extern __shared__ __align__(128) uint8_t po_smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mt = warp % MT, kw = warp / MT;
-    const int rank = (int)blockIdx.x % a.ranks, unit = (int)blockIdx.x / a.ranks;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int split = (int)blockIdx.x % a.splits, unit = (int)blockIdx.x / a.splits;
     const int j = unit % a.Hkv, b = unit / a.Hkv;
-    const int n = a.S > 0 ? seq_len(a.lens, b, a.S) : 0;
+    const int n = seq_len(a.lens, b, a.S);
     const int R = a.Lq * a.G;
     auto row_of = [&](int r) { return ((long long)b * a.Lq + r / a.G) * a.Hq + j * a.G + r % a.G; };
     // stage st of warp w of this key stream (its block of a set)
     auto stage = [&](int w, int st) { return smem_u32(po_smem) + (kw * MT + w) * S::WARP + st * S::STAGE; };
 
     // sets x = sid, sid + streams, ... of MT blocks
-    const int nset = (n + MT * PO_BLOCK - 1) / (MT * PO_BLOCK), streams = a.ranks * KW, sid = rank * KW + kw;
+    const int nset = (n + MT * PO_BLOCK - 1) / (MT * PO_BLOCK), streams = a.splits * KW, sid = split * KW + kw;
     const int niter = nset > sid ? (nset - sid + streams - 1) / streams : 0;
     const long long krow = (long long)a.Hkv * D;                     // elements from key to key
     const __nv_bfloat16* kb = a.k + ((long long)b * a.S * a.Hkv + j) * D + (lane % CPR) * 8;
@@ -215,7 +212,6 @@ prefix_own_kernel(const PrefixOwnArgs a) {
     float* mo = reinterpret_cast<float*>(po_smem);
     float* ml = reinterpret_cast<float*>(po_smem + S::MERGE_ML);
     float* row_lse = reinterpret_cast<float*>(po_smem + S::LSE);
-    float* scr = reinterpret_cast<float*>(po_smem + S::SCR);
 #pragma unroll
     for (int x = 0; x < D / 8; ++x) {
         *reinterpret_cast<float2*>(mo + (warp * 16 + g) * S::MROW + x * 8 + cq) = make_float2(o[x][0], o[x][1]);
@@ -248,9 +244,10 @@ prefix_own_kernel(const PrefixOwnArgs a) {
         row_lse[tid] = L == 0.0f ? -INFINITY : (M == -INFINITY ? L : M + log2f(L));
     }
     __syncthreads();
-    // key stream 0's copy of the row (warp r / 16) is overwritten by the result
-    for (int e = tid; e < MT * 16 * (D / 4); e += PO_THREADS) {
+    for (int e = tid; e < R * (D / 4); e += PO_THREADS) {
         const int r = e / (D / 4), c = e % (D / 4) * 4;
+        const long long row = row_of(r);
+        const float l = row_lse[r];
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
@@ -261,126 +258,19 @@ prefix_own_kernel(const PrefixOwnArgs a) {
             acc.z = fmaf(f, v.z, acc.z);
             acc.w = fmaf(f, v.w, acc.w);
         }
-        *reinterpret_cast<float4*>(mo + r * S::MROW + c) = acc;
+        if (a.to_parts) {
+            const long long at = row * a.slots + a.slot0 + split;
+            if (c == 0) a.part_lse[at] = l;
+            // an empty partial's values are not read
+            if (l != -INFINITY) *reinterpret_cast<float4*>(a.part_o + at * D + c) = acc;
+        } else {
+            *reinterpret_cast<uint2*>(a.out + row * D + c) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+            if (c == 0 && a.lse) a.lse[row] = l * LN2;
+        }
     }
-    if (a.ranks > 1) cluster_sync();
-    else __syncthreads();
-
-    // ---------------- the row over all ranks and prefix partials
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    // A row's items are the ranks' results and its prefix partials, taken eight
-    // at a time with an online softmax over their log2-sum-exps.  Loads are
-    // unconditional (past the end: the last item again): loads behind branches
-    // ran one after the other.  Four warps share a single row, two share each
-    // of two or three, a warp takes one of more.
-    constexpr int E = D / 32, UN = 8;                                // columns a lane, items at once (ranks <= 8)
-    const int my_rows = (R - rank + a.ranks - 1) / a.ranks;          // rows rank, rank + ranks, ...
-    const int gw = my_rows >= 4 ? 1 : my_rows >= 2 ? 2 : 4, sub = warp % gw;
-    float M, W, acc[E];
-    auto add = [&](const float (&l)[UN], const float (&v)[UN][E]) {
-        float bm = M;
-#pragma unroll
-        for (int u = 0; u < UN; ++u) bm = fmaxf(bm, l[u]);
-        const float al = M == -INFINITY ? 0.0f : sa_ex2(M - bm);     // nothing was added while M was -inf
-        if (M != -INFINITY) W *= al;                                 // (or sums that are not numbers, which stay)
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] *= al;
-#pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const float w = l[u] == -INFINITY ? 0.0f : sa_ex2(l[u] - bm);
-            W += w;
-            // an empty partial's values are not written: they may be anything
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(w, w == 0.0f ? 0.0f : v[u][e], acc[e]);
-        }
-        M = bm;
-    };
-    auto finish = [&](long long row, float M, float W, const float (&acc)[E]) {
-        const float inv = W == 0.0f ? 0.0f : 1.0f / W;
-        uint32_t w[E / 2];
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) w[e] = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + lane * E);
-        if (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[E / 2 - 1]);
-        else dst[0] = w[0];
-        if (a.lse && lane == 0) a.lse[row] = W == 0.0f ? -INFINITY : (M == -INFINITY ? W : M + log2f(W)) * LN2;
-    };
-    for (int r0 = rank; r0 < R; r0 += a.ranks * (4 / gw)) {
-        const int r = r0 + warp / gw * a.ranks;
-        const bool on = r < R;                                       // uniform over the warp
-        const long long row = row_of(on ? r : rank);
-        M = -INFINITY;
-        W = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-        if (on && sub == 0) {
-            float l[UN], v[UN][E];
-            const float* src = mo + r * S::MROW + lane * E;
-            if (a.ranks > 1) {
-#pragma unroll
-                for (int x = 0; x < UN; ++x) {
-                    const uint32_t from = (uint32_t)min(x, a.ranks - 1);
-                    l[x] = __uint_as_float(ld_dsmem_u32(smem_u32(row_lse + r), from));
-                    ld_dsmem(smem_u32(src), from, v[x]);
-                }
-            } else {
-#pragma unroll
-                for (int x = 0; x < UN; ++x) {
-                    l[x] = row_lse[r];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) v[x][e] = src[e];
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < UN; ++x)
-                if (x >= a.ranks) l[x] = -INFINITY;
-            add(l, v);
-        }
-        if (on) {
-            const float* pl = a.part_lse + row * a.slots;
-            const float* po = a.part_o + row * a.slots * D + lane * E;
-            for (int s0 = sub * UN; s0 < a.slots; s0 += gw * UN) {
-                float l[UN], v[UN][E];
-#pragma unroll
-                for (int u = 0; u < UN; ++u) {
-                    const int x = min(s0 + u, a.slots - 1);
-                    l[u] = pl[x];
-                    const float* src = po + (long long)x * D;
-                    if (E == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src);
-                    else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src);
-                }
-#pragma unroll
-                for (int u = 0; u < UN; ++u)
-                    if (s0 + u >= a.slots) l[u] = -INFINITY;
-                add(l, v);
-            }
-        }
-        if (gw > 1) {                                                // uniform over the CTA
-            // the group's warps meet in shared memory; its first one finishes
-            __syncthreads();
-#pragma unroll
-            for (int e = 0; e < E; ++e) scr[warp * D + lane * E + e] = acc[e];
-            if (lane == 0) *reinterpret_cast<float2*>(scr + 4 * D + 2 * warp) = make_float2(M, W);
-            __syncthreads();
-            if (sub == 0) {
-                float l[UN], v[UN][E];
-#pragma unroll
-                for (int u = 0; u < UN; ++u) {
-                    const int w = warp + min(u, gw - 1);
-                    const float2 mw = *reinterpret_cast<const float2*>(scr + 4 * D + 2 * w);
-                    // as one item: its values over W, its log2-sum-exp (or what is not a number)
-                    const bool more = u > 0 && u < gw;
-                    l[u] = !more || mw.y == 0.0f ? -INFINITY : mw.x == -INFINITY ? mw.y : mw.x + log2f(mw.y);
-                    const float inv = more && mw.y != 0.0f ? 1.0f / mw.y : 0.0f;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) v[u][e] = scr[w * D + lane * E + e] * inv;
-                }
-                add(l, v);
-            }
-        }
-        if (on && sub == 0) finish(row, M, W, acc);
-    }
-    if (a.ranks > 1) cluster_sync();       // no CTA leaves while another may read its shared memory
+    // The grid ends after the prefix kernel it depends on, so that the merge,
+    // which waits for this grid, has both; one CTA -- the last to start -- sees to it.
+    if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace ic
