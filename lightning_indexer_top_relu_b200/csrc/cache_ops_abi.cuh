@@ -101,13 +101,18 @@ struct PrefixGeom {
     size_t ws_bytes = 0;
 };
 
-// How finely the keys are split, and whether two row tiles share a CTA: `s`
-// bounds the steps (one stream's 128 rows x 128 keys, about 0.9 us) of a unit,
-// and the s of the smallest estimated time is taken.  A unit costs its steps
-// and 6 to 7.5 more to start and to write its partials (a shared unit writes
-// twice as many); an own tile counts double (64 KB of K and V for one step); a
-// partial row also costs its reading by the merge.  Units up to the number of SMs
-// run at once, more run in turn, the last half a unit late on average.
+// How finely the keys are split, and whether two row tiles share a CTA: every
+// number of splits is tried and the smallest estimated time taken.  In us, as
+// measured: 1.05 a step (one stream's 128 rows x 128 keys; 0.95 in a shared unit,
+// whose streams take turns and read half as much), 6 to start a unit and write
+// its partials, 8 for a shared one, which writes twice as many rows; 2 for
+// each 32 partials a row has to merge; an own tile as a unit counts two
+// steps.  Units up to the number of SMs run at once, more run in turn, the last
+// half a unit late on average.  The own-cache kernel reads 40 GB/s an SM (caches
+// taken as three quarters full), on SMs without a unit first.
+//   32 sequences, 32K prefix, caches of 2K: 104 split units of 10 steps 26.6 us,
+//   148 of 7 steps 31.1, 104 shared ones of 10 steps 28.3; without own caches
+//   128 split units of 8 steps 22.7, 148 of 7 steps 24.5.
 PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int sms) {
     PrefixGeom g;
     const int T = ic::PA_KEYS, R = ic::PA_ROWS, G = Hq / Hkv;
@@ -131,23 +136,32 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
     const int own_slots = g.o_splits;
     if (has_o) g.o_row_units = (int)((ro + R - 1) / R);
     const long long n_ou = (long long)B * g.o_row_units * Hkv;
-    const double o_work = 2.0 * n_ou * o_nt, row_bytes = (double)B * Lq * Hq * d * 4.0;
+    const double own_us = g.own_kernel ? 0.75 * B * S * Hkv * d * 4.0 / 40e3 : 0.0;   // of one SM
     double best = -1.0;
     for (int shared = 0; shared <= (rp > R ? 1 : 0); ++shared) {
         const int per_step = shared ? 2 : 1;
         const int row_units = has_p ? (int)((rp + R * per_step - 1) / (R * per_step)) : 0;
         const long long n_pu = (long long)row_units * Hkv;
-        const double p_work = (double)n_pu * p_nt * per_step, ends = shared ? 7.5 : 6.0;
-        const int s_max = std::max(has_p ? p_nt * per_step : 1, has_o ? o_nt : 1);
-        for (int s = 1;; s = std::min(s_max, s + std::max(1, s / 8))) {
-            const int p_tps = std::min(std::max(1, s / per_step), std::max(1, p_nt));
-            const int o_tps = std::min(std::max(1, s / 2), o_nt);
+        const double ends = shared ? 8.0 : 6.0, step_us = shared ? 0.95 : 1.05;
+        // tiles a split (own units, where this kernel has them, as many steps):
+        // the values that some number of splits gives, about 2 sqrt(nt) of them
+        const int nt = has_p ? p_nt : o_nt;
+        auto fewer = [&](int tps) {                                // what one split more gives, if that is less
+            const int k = (nt + tps - 1) / tps + 1;
+            return std::min(tps - 1, (nt + k - 1) / k);
+        };
+        for (int tps = nt; tps >= 1; tps = fewer(tps)) {
+            const int p_tps = has_p ? tps : 0;
+            const int steps = has_p ? p_tps * per_step : 2 * tps;
+            const int o_tps = std::min(std::max(1, steps / 2), o_nt);
             const int p_sp = has_p ? (p_nt + p_tps - 1) / p_tps : 0, o_sp = has_o ? (o_nt + o_tps - 1) / o_tps : 0;
             const long long slots = (long long)p_sp + o_sp + own_slots;
             const double n = (double)n_pu * p_sp + (double)n_ou * o_sp;
-            const double unit = ends + std::max(has_p ? p_tps * per_step : 0, has_o ? 2 * o_tps : 0);
-            double est = n <= sms ? unit : std::max(unit, (p_work + o_work + ends * n) / sms + 0.5 * unit);
-            if (slots > 1) est += row_bytes * slots * 3.0e-7;
+            const double work = step_us * ((double)n_pu * p_nt * per_step + 2.0 * n_ou * o_nt) + ends * n;
+            const double unit = ends + step_us * std::max(steps, has_o ? 2 * o_tps : 0);
+            double est = n <= sms ? unit : std::max(unit, work / sms + 0.5 * unit);
+            est += std::max(0.0, own_us - std::max(0.0, sms - n) * unit) / sms;
+            if (slots > 1) est += 2.0 * ((slots + 31) / 32);
             if (n < 2147483647.0 && (best < 0.0 || est < best)) {
                 best = est;
                 g.shared = shared != 0;
@@ -159,7 +173,6 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
                 g.n_prefix = n_pu * p_sp;
                 g.n_own = n_ou * o_sp;
             }
-            if (s >= s_max) break;
         }
     }
     if (g.slots > 1) g.ws_bytes = (size_t)B * Lq * Hq * g.slots * (d + 1) * sizeof(float);
