@@ -41,6 +41,8 @@
  *       - the other fp32 / int32 buffers (scores, idx, lse, counts) must be
  *         4-byte aligned.
  *     A misaligned pointer returns IC_ERR_UNSUPPORTED before any launch.
+ *   - A call writes its workspace: calls that may run at the same time (on
+ *     several streams, or captured graphs replayed side by side) need one each.
  *   - Device-side faults are never raised on purpose: kernels report an
  *     out-of-range attention index or a timed-out wait into a device error
  *     word that ic_get_last_device_error() reads.
@@ -446,7 +448,8 @@ size_t ic_attn_mass_sparse_workspace_bytes(int B, int Lq, int Lk);
  * those first in the order (mass descending, position ascending; NaN ranks as
  * -INFINITY).  Positions are written ascending, then -1.  new_lens[b] =
  * min(n, n_keep).  n_sink + n_recent <= n_keep.  A length outside [0, Lk] is
- * clamped and flags IC_ERR_INVALID_ARG in the device error word.  B <= 65535.  Exact.
+ * clamped and flags IC_ERR_INVALID_ARG in the device error word.  B <= 65535,
+ * Lk and n_keep <= 2^30.  Exact.
  */
 int ic_evict_select(const float *mass, const int32_t *lens, int B, int Lk, int n_keep, int n_sink,
                     int n_recent, int32_t *keep, int32_t *new_lens, ic_stream_t stream);

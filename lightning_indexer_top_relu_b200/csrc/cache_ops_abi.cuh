@@ -478,7 +478,9 @@ int ic_evict_select(const float* mass, const int32_t* lens, int B, int Lk, int n
     if ((Lk > 0 && !mass) || !keep) return fail(IC_ERR_INVALID_ARG, "null pointer");
     if (!aligned4(mass) || !aligned4(lens) || !aligned4(keep) || !aligned4(new_lens))
         return fail(IC_ERR_UNSUPPORTED, "mass, lens, keep and new_lens must be 4-byte aligned");
-    if (B > 65535) return fail(IC_ERR_UNSUPPORTED, "B=%d (supported: up to 65535)", B);
+    if (B > 65535 || Lk > (1 << 30) || n_keep > (1 << 30))
+        return fail(IC_ERR_UNSUPPORTED, "B=%d Lk=%d n_keep=%d (supported: B <= 65535, Lk and n_keep <= 2^30)", B,
+                    Lk, n_keep);
     int dev, sms;
     int rc = device_setup(&dev, &sms);
     if (rc) return rc;

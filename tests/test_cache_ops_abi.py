@@ -98,7 +98,7 @@ def test_evict_select_refusals(ic):
     assert call(n_keep=0) == 1 and call(n_keep=3) == 1         # below n_sink + n_recent
     assert call(mass=None) == 1 and call(keep=None) == 1
     assert call(mass=0x1002) == 2 and call(keep=0x2001) == 2 and call(new=0x3002) == 2
-    assert call(B=70000) == 2
+    assert call(B=70000) == 2 and call(Lk=(1 << 30) + 1) == 2 and call(n_keep=(1 << 30) + 1) == 2
     assert call(B=0) == 0
 
 

@@ -535,3 +535,130 @@ def test_graph_replay_and_side_stream(ic):
         for a, b in zip(eager, captured):
             assert torch.equal(a, b)
     del graph
+
+
+def test_no_keys_at_all(ic):
+    q = randn(gen(14), 3, 2, 8, 64).bfloat16()
+    none = torch.empty(0, 1, 64, device="cuda", dtype=torch.bfloat16)
+    for own in ((None, None), (torch.empty(3, 0, 1, 64, device="cuda", dtype=torch.bfloat16),) * 2):
+        out, lse = ic.prefix_attn(q, none, none, *own, out=torch.full_like(q, 7))
+        ok(ic)
+        assert (out == 0).all() and (lse == -INF).all()
+    mass = torch.ones(3, 0, device="cuda")
+    assert ic.attn_mass(q, own[0], lse, mass) is mass
+    keep, n = ic.evict_select(torch.empty(2, 0, device="cuda"), 3)
+    ok(ic)
+    assert (keep == -1).all() and n.tolist() == [0, 0]
+
+
+def test_operands_elsewhere_or_strided_are_refused(ic):
+    q = randn(gen(15), 2, 4, 16, 128).bfloat16()
+    kp = randn(gen(16), 64, 128).bfloat16()
+    with pytest.raises(ValueError, match="contiguous"):
+        ic.prefix_attn(q.transpose(0, 1), kp, kp)
+    with pytest.raises(ValueError, match="contiguous"):
+        ic.prefix_attn(q, kp[::2], kp[::2])
+    with pytest.raises(TypeError, match="bfloat16"):
+        ic.prefix_attn(q.float(), kp, kp)
+    with pytest.raises(ValueError, match="CUDA"):
+        ic.prefix_attn(q, kp.cpu(), kp)
+    mass = torch.zeros(2, 64, device="cuda")
+    with pytest.raises(TypeError, match="float32"):
+        ic.evict_select(mass.double(), 4)
+    with pytest.raises(ValueError, match="contiguous"):
+        ic.cache_gather(torch.zeros(2, 3, device="cuda", dtype=torch.int32), [mass], [mass.t().clone().t()[:, :3]])
+
+
+def test_two_streams_at_once(ic):
+    """Calls over different inputs on two streams, each with its own
+    workspace, give what they give alone."""
+    runs = []
+    for seed, B, P, S in ((17, 20, 5000, 300), (18, 7, 9000, 700)):
+        g = gen(seed)
+        q = randn(g, B, 1, 16, 128).bfloat16()
+        kp, vp = randn(g, P, 1, 128).bfloat16(), randn(g, P, 1, 128).bfloat16()
+        k, v = randn(g, B, S, 1, 128).bfloat16(), randn(g, B, S, 1, 128).bfloat16()
+        lens = torch.randint(1, S + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+
+        def step(q=q, kp=kp, vp=vp, k=k, v=v, lens=lens, B=B, P=P, S=S):
+            out, lse = ic.prefix_attn(q, kp, vp, k, v, lens)
+            mass = torch.zeros(1, P, device="cuda")
+            ic.attn_mass(q.view(1, B, 16, 128), kp.view(1, P, 1, 128), lse.view(1, B, 16), mass, q_offset=P)
+            keep, _ = ic.evict_select(mass, P // 3, n_sink=4, n_recent=100)
+            dst = torch.zeros(1, P // 3, 1, 128, device="cuda", dtype=torch.bfloat16)
+            ic.cache_gather(keep, [kp.view(1, P, 1, 128)], [dst])
+            return out, lse, mass, keep, dst
+        runs.append(step)
+    torch.cuda.synchronize()
+    alone = [step() for step in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(3):
+        got = []
+        for s, step in zip(streams, runs):
+            with torch.cuda.stream(s):
+                got.append(step())
+    ok(ic)
+    for a, b in zip(alone, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+def test_offsets_past_32_bits(ic):
+    """Caches of more than 2^31 elements (4.3 GB): rows at the far end are
+    the ones attended, weighed, kept and moved."""
+    L, d = (1 << 24) + 4099, 128
+    k = torch.zeros(1, L, 1, d, device="cuda", dtype=torch.bfloat16)
+    v = torch.zeros(1, L, 1, d, device="cuda", dtype=torch.bfloat16)
+    g = gen(19)
+    q = randn(g, 1, 1, 16, d).bfloat16()
+    far = L - 3
+    k[0, far, 0] = 8 * q[0, 0].float().mean(0).bfloat16()
+    k[0, far - 1] = k[0, far]
+    v[0, far, 0] = randn(g, d).bfloat16()
+    for own in (False, True):
+        if own:
+            none = torch.empty(0, 1, d, device="cuda", dtype=torch.bfloat16)
+            out, lse = ic.prefix_attn(q, none, none, k, v)
+        else:
+            out, lse = ic.prefix_attn(q, k[0], v[0])
+        ok(ic)
+        z = (q[0, 0].double() @ k[0, far, 0].double()) * d ** -0.5            # two such keys, the others score 0
+        den = 2 * torch.exp(z) + (L - 2)
+        ref = (torch.exp(z) / den)[:, None] * v[0, far, 0].double()
+        assert (lse[0, 0].double() - torch.log(den)).abs().max() <= 1e-4
+        assert ((out[0, 0].double() - ref).abs() <= 2.0 ** -7 * ref.abs() + 1e-30).all()
+    del v
+    mass = torch.zeros(1, L, device="cuda")
+    ic.attn_mass(q, k, lse, mass, q_offset=L - 1)
+    w = torch.exp(z - lse[0, 0].double()).sum()
+    ok(ic)
+    assert abs(mass[0, far].item() / w.item() - 1) <= 1e-4 and mass[0, far] == mass[0, far - 1]
+    idx = torch.tensor([[[far - 1, far, 5]]], device="cuda", dtype=torch.int32)
+    sparse = ic.attn_mass_sparse(q, k, idx, lse, torch.zeros(1, L, device="cuda"), q_offset=L - 1)
+    ok(ic)
+    assert abs(sparse[0, far].item() / w.item() - 1) <= 1e-4 and sparse.count_nonzero() == 3
+    mass[0, 7] = 2 * mass[0, far]
+    keep, _ = ic.evict_select(mass, 3)
+    dst = torch.ones(1, 3, 1, d, device="cuda", dtype=torch.bfloat16)
+    ic.cache_gather(keep, [k], [dst])
+    ok(ic)
+    assert keep[0].tolist() == [7, far - 1, far]
+    assert torch.equal(dst[0, 1:], k[0, far - 1:far + 1]) and (dst[0, 0] == 0).all()
+
+
+def test_a_query_that_is_not_a_number_spoils_its_row_alone(ic):
+    g = gen(20)
+    q = randn(g, 12, 1, 16, 128).bfloat16()
+    kp, vp = randn(g, 3000, 1, 128).bfloat16(), randn(g, 3000, 1, 128).bfloat16()
+    k, v = randn(g, 12, 90, 1, 128).bfloat16(), randn(g, 12, 90, 1, 128).bfloat16()
+    a, la = ic.prefix_attn(q, kp, vp, k, v)
+    bad = q.clone()
+    bad[5, 0, 3, 17] = float("nan")
+    b, lb = ic.prefix_attn(bad, kp, vp, k, v)
+    ok(ic)
+    rest = torch.ones(12, 1, 16, dtype=torch.bool, device="cuda")
+    rest[5, 0, 3] = False
+    assert torch.isnan(b[5, 0, 3]).all() and torch.isnan(lb[5, 0, 3])
+    assert torch.equal(a[rest], b[rest]) and torch.equal(la[rest], lb[rest])
