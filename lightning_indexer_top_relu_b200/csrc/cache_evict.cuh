@@ -29,8 +29,9 @@
 
 namespace ic {
 
-constexpr int EV_THREADS = 512;
-constexpr int EV_WARPS = EV_THREADS / 32;
+// Threads a CTA: 512, two CTAs an SM; 1024 for slices over 8K positions, whose
+// passes over shared memory are bound by issue (two 500K caches: 36 -> 32 us).
+constexpr int EV_THREADS = 512, EV_THREADS_LONG = 1024, EV_LONG = 8192;
 constexpr int EV_BINS = 256;                 // 8 bits a pass
 constexpr int EV_CACHE_MAX = 40960;          // keys of a slice kept in shared memory
 constexpr int EV_CLUSTER_MAX = 16;           // above 8 where the device has room for such a cluster
@@ -47,8 +48,8 @@ struct EvictArgs {
 
 struct EvictSmem {
     static constexpr int OFF_HIST = 0;                               // [4][256]
-    static constexpr int OFF_WARP = OFF_HIST + 4 * EV_BINS * 4;      // [16] u64 per-warp sums
-    static constexpr int OFF_FOUND = OFF_WARP + EV_WARPS * 8;        // bin, above, lower above, lower at
+    static constexpr int OFF_WARP = OFF_HIST + 4 * EV_BINS * 4;      // [32] u64 per-warp sums
+    static constexpr int OFF_FOUND = OFF_WARP + 32 * 8;        // bin, above, lower above, lower at
     static constexpr int OFF_KEYS = OFF_FOUND + 16;
     static constexpr int bytes(int keys) { return OFF_KEYS + keys * 4; }
 };
@@ -81,6 +82,7 @@ __device__ __forceinline__ void cluster_or_block_sync(int C) {
 
 // Exclusive prefix over the block of one 64-bit value a thread (two 32-bit
 // counts); `sums` is scratch of one value a warp.
+template <int NW>
 __device__ __forceinline__ unsigned long long ev_block_prefix(unsigned long long mine, unsigned long long* sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned long long x = mine;
@@ -91,9 +93,9 @@ __device__ __forceinline__ unsigned long long ev_block_prefix(unsigned long long
     }
     if (lane == 31) sums[warp] = x;
     __syncthreads();
-    unsigned long long s = lane < EV_WARPS ? sums[lane] : 0ull;
+    unsigned long long s = lane < NW ? sums[lane] : 0ull;
 #pragma unroll
-    for (int o = 1; o < EV_WARPS; o <<= 1) {
+    for (int o = 1; o < NW; o <<= 1) {
         const unsigned long long y = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += y;
     }
@@ -101,9 +103,11 @@ __device__ __forceinline__ unsigned long long ev_block_prefix(unsigned long long
     return (warp > 0 ? before : 0ull) + x - mine;
 }
 
-__global__ void __launch_bounds__(EV_THREADS)
+template <int NT>
+__global__ void __launch_bounds__(NT)
 evict_select_kernel(const EvictArgs a) {
     using S = EvictSmem;
+    constexpr int NW = NT / 32;
     extern __shared__ __align__(16) uint8_t ev_smem[];
     uint32_t* hist = reinterpret_cast<uint32_t*>(ev_smem + S::OFF_HIST);
     unsigned long long* sums = reinterpret_cast<unsigned long long*>(ev_smem + S::OFF_WARP);
@@ -115,7 +119,7 @@ evict_select_kernel(const EvictArgs a) {
     int32_t* keep = a.keep + (long long)b * a.n_keep;
     if (rank == 0 && tid == 0 && a.new_lens) a.new_lens[b] = min(n, a.n_keep);
     if (n <= a.n_keep) {                                             // uniform over the cluster
-        for (int j = rank * EV_THREADS + tid; j < a.n_keep; j += C * EV_THREADS) keep[j] = j < n ? j : -1;
+        for (int j = rank * NT + tid; j < a.n_keep; j += C * NT) keep[j] = j < n ? j : -1;
         return;
     }
     // middle positions [n_sink, n - n_recent), at least one more than the kk kept of them
@@ -127,10 +131,10 @@ evict_select_kernel(const EvictArgs a) {
     const float* src = a.mass + (long long)b * a.Lk + a.n_sink + lo;
 
     if (rank == 0)
-        for (int j = tid; j < a.n_sink; j += EV_THREADS) keep[j] = j;
+        for (int j = tid; j < a.n_sink; j += NT) keep[j] = j;
     if (rank == C - 1)
-        for (int j = tid; j < a.n_recent; j += EV_THREADS) keep[a.n_keep - a.n_recent + j] = n - a.n_recent + j;
-    for (int e = tid; e < 4 * EV_BINS; e += EV_THREADS) hist[e] = 0u;
+        for (int j = tid; j < a.n_recent; j += NT) keep[a.n_keep - a.n_recent + j] = n - a.n_recent + j;
+    for (int e = tid; e < 4 * EV_BINS; e += NT) hist[e] = 0u;
     __syncthreads();
 
     uint32_t prefix = 0;                     // the key bits fixed so far
@@ -141,12 +145,12 @@ evict_select_kernel(const EvictArgs a) {
         const int shift = 24 - 8 * pass;
         uint32_t* h = hist + pass * EV_BINS;
         const bool global = pass == 0 || !a.cached;
-        for (int e0 = 0; e0 < m; e0 += EV_THREADS * EV_BATCH) {
+        for (int e0 = 0; e0 < m; e0 += NT * EV_BATCH) {
             uint32_t key[EV_BATCH];
-            ev_load(key, global, src, keys, e0 + tid, EV_THREADS, m);
+            ev_load(key, global, src, keys, e0 + tid, NT, m);
 #pragma unroll
             for (int u = 0; u < EV_BATCH; ++u) {
-                const int e = e0 + u * EV_THREADS + tid;
+                const int e = e0 + u * NT + tid;
                 if (e < m) {
                     if (pass == 0 && a.cached) keys[e] = key[u];
                     // (no vote on equal bins first: adds of one constant to one address combine)
@@ -175,7 +179,7 @@ evict_select_kernel(const EvictArgs a) {
                 }
             }
         }
-        const unsigned long long above = ev_block_prefix((unsigned long long)lower << 32 | all, sums);
+        const unsigned long long above = ev_block_prefix<NW>((unsigned long long)lower << 32 | all, sums);
         if ((uint32_t)above < (uint32_t)remaining && (uint32_t)above + all >= (uint32_t)remaining) {
             found[0] = (uint32_t)(EV_BINS - 1 - tid);
             found[1] = (uint32_t)above;
@@ -195,7 +199,7 @@ evict_select_kernel(const EvictArgs a) {
     const int need = remaining;                          // keys equal to T kept, lowest positions first
 
     // each warp owns a contiguous segment of the slice
-    const int seg = ((m + EV_WARPS - 1) / EV_WARPS + 31) / 32 * 32;
+    const int seg = ((m + NW - 1) / NW + 31) / 32 * 32;
     const int w0 = min(warp * seg, m), w1 = min(w0 + seg, m);
     uint32_t gt = 0, eq = 0;
     for (int e0 = w0; e0 < w1; e0 += 32 * EV_BATCH) {
@@ -209,7 +213,7 @@ evict_select_kernel(const EvictArgs a) {
         }
     }
     // a thread's share of the block's counts; a warp's first lane has the sum before it
-    const unsigned long long before = ev_block_prefix((unsigned long long)eq << 32 | gt, sums);
+    const unsigned long long before = ev_block_prefix<NW>((unsigned long long)eq << 32 | gt, sums);
     uint32_t gt_before = gt_lower + (uint32_t)__shfl_sync(0xffffffffu, before, 0);
     uint32_t eq_before = eq_lower + (uint32_t)(__shfl_sync(0xffffffffu, before, 0) >> 32);
     const uint32_t lt = (1u << lane) - 1u;

@@ -495,7 +495,8 @@ int ic_evict_select(const float* mass, const int32_t* lens, int B, int Lk, int n
     a.cached = per <= ic::EV_CACHE_MAX ? 1 : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)C, (unsigned)B);
-    cfg.blockDim = dim3(ic::EV_THREADS);
+    const bool longer = per > ic::EV_LONG;
+    cfg.blockDim = dim3(longer ? ic::EV_THREADS_LONG : ic::EV_THREADS);
     cfg.dynamicSmemBytes = ic::EvictSmem::bytes(a.cached ? per : 0);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute at[1];
@@ -505,7 +506,9 @@ int ic_evict_select(const float* mass, const int32_t* lens, int B, int Lk, int n
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return launched(cudaLaunchKernelEx(&cfg, ic::evict_select_kernel, a), "evict_select launch");
+    return launched(cudaLaunchKernelEx(&cfg, longer ? ic::evict_select_kernel<ic::EV_THREADS_LONG>
+                                                    : ic::evict_select_kernel<ic::EV_THREADS>, a),
+                    "evict_select launch");
 }
 
 int ic_cache_gather(const int32_t* keep, int B, int Lk, int n_keep, int Lk_dst, int n_tensors,

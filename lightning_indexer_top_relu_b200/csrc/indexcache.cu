@@ -372,13 +372,14 @@ bool attn_cluster_fits() {
 }
 
 // Whether clusters of c CTAs of the eviction select with full slices fit.
+template <int NT>
 bool evict_cluster_fits(int c) {
-    if (c > 8 && cudaFuncSetAttribute(ic::evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-                     cudaSuccess)
+    if (c > 8 && cudaFuncSetAttribute(ic::evict_select_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                      1) != cudaSuccess)
         return false;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)c, 1, 1);
-    cfg.blockDim = dim3(ic::EV_THREADS, 1, 1);
+    cfg.blockDim = dim3(NT, 1, 1);
     cfg.dynamicSmemBytes = ic::EvictSmem::bytes(ic::EV_CACHE_MAX);
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -388,7 +389,10 @@ bool evict_cluster_fits(int c) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, ic::evict_select_kernel, &cfg) == cudaSuccess && n > 0;
+    return cudaOccupancyMaxActiveClusters(&n, ic::evict_select_kernel<NT>, &cfg) == cudaSuccess && n > 0;
+}
+bool evict_cluster_fits_all(int c) {
+    return evict_cluster_fits<ic::EV_THREADS>(c) && evict_cluster_fits<ic::EV_THREADS_LONG>(c);
 }
 
 template <int D>
@@ -845,13 +849,15 @@ int device_setup(int* dev_out, int* sms_out) {
                              ic::AM_SMEM);
         cudaFuncSetAttribute(ic::attn_mass_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ic::AM_SMEM);
-        cudaFuncSetAttribute(ic::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(ic::evict_select_kernel<ic::EV_THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ic::EvictSmem::bytes(ic::EV_CACHE_MAX));
+        cudaFuncSetAttribute(ic::evict_select_kernel<ic::EV_THREADS_LONG>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, ic::EvictSmem::bytes(ic::EV_CACHE_MAX));
         e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
         g_attn_cluster[dev] = attn_cluster_fits<64>() && attn_cluster_fits<128>();
-        g_evict_cluster[dev] = evict_cluster_fits(ic::EV_CLUSTER_MAX) ? ic::EV_CLUSTER_MAX
-                               : evict_cluster_fits(8) ? 8 : 1;
+        g_evict_cluster[dev] = evict_cluster_fits_all(ic::EV_CLUSTER_MAX) ? ic::EV_CLUSTER_MAX
+                               : evict_cluster_fits_all(8) ? 8 : 1;
         cudaGetLastError();                         // a refused query only disables clusters
         g_sms[dev] = sms;
         g_attr_done[dev] = true;
