@@ -24,8 +24,8 @@
 // row j.  Bound by memory bandwidth.
 #pragma once
 
+#include "cache_util.cuh"
 #include "common.cuh"
-#include "prefix_attn.cuh"
 
 namespace ic {
 

@@ -18,7 +18,6 @@ enum : unsigned int {
     DEV_ERR_TIMEOUT = 1u,     // a bounded wait gave up
     DEV_ERR_BAD_INDEX = 2u,   // an attention index outside [0, t] (skipped)
     DEV_ERR_SMEM = 4u,        // the 1024-aligned shared-memory layout did not fit (kernel skipped)
-    DEV_ERR_BAD_LENGTH = 8u,  // a sequence length outside [0, capacity] (clamped)
 };
 
 constexpr int MAX_DYN_SMEM = 232448;          // 227 KB opt-in per CTA on sm_100
@@ -270,60 +269,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 // Named barrier among a subset of warps (id 1..15).
 __device__ __forceinline__ void named_bar(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
-// Arrives at a named barrier without waiting for it.
-__device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
-// True in one lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r != 0;
-}
-
-// A value that is the same in all lanes, in a form the compiler can keep in
-// uniform registers.
-template <typename T>
-__device__ __forceinline__ T warp_uniform(T v) {
-    return __shfl_sync(0xffffffffu, v, 0);
-}
-
-// As named_bar; returns whether any of the threads passed a true `v`.
-__device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %3, 0;\n\t"
-        "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(nthreads), "r"((uint32_t)v)
-        : "memory");
-    return r != 0;
-}
-
-// Thread-block clusters: a barrier over the cluster's CTAs (shared-memory
-// writes before it are visible to the others after it) and loads from another
-// CTA's shared memory.
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t local_addr, uint32_t rank) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_addr), "r"(rank));
-    return remote;
-}
-__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t local_addr, uint32_t rank) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(local_addr, rank)) : "memory");
-    return v;
 }
 
 }  // namespace ic

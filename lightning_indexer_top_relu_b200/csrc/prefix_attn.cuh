@@ -45,6 +45,7 @@
 // instructions.
 #pragma once
 
+#include "cache_util.cuh"
 #include "common.cuh"
 #include "dense_attn.cuh"
 
@@ -77,18 +78,6 @@ struct PrefixAttnArgs {
     float scale_log2;
 };
 
-// Positions of its own cache that sequence b holds; a length outside [0, cap]
-// is clamped and reported.
-__device__ __forceinline__ int seq_len(const int32_t* lens, int b, int cap) {
-    if (lens == nullptr) return cap;
-    const int n = __ldg(lens + b);
-    if (n < 0 || n > cap) {
-        report(DEV_ERR_BAD_LENGTH);
-        return n < 0 ? 0 : cap;
-    }
-    return n;
-}
-
 template <int D>
 struct PrefixSmem {
     static constexpr int QTILE = PA_ROWS * D * 2;            // one row tile (D / 64 boxes)
@@ -104,64 +93,6 @@ struct PrefixSmem {
     static constexpr int ALLOC = BYTES + 1024;               // slack for the 1024-byte alignment
     static_assert(ALLOC <= MAX_DYN_SMEM, "shared memory of one CTA");
 };
-
-// Waits for the loads of tcgen05.ld into r: the registers pass through, so no
-// use of them moves ahead of the wait.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
-                   "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
-                   "+r"(r[31])::"memory");
-}
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
-                                            int y, int z, int w) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-        : "memory");
-}
-
-// Shared-memory matrix descriptors as {low, high} words, so that stepping
-// through a tile is one 32-bit add of bytes / 16 to the low word.  High word:
-// stride byte offset 1024 (the next 8 rows of 128 B), version 1, 128-byte
-// swizzle.  Low word: address / 16 and the leading byte offset -- for a K-major
-// operand unused (1), for an MN-major one (64 MN elements x 8 K rows per
-// 1024-byte atom) the distance of the next 64 MN elements, one TMA box on.
-constexpr uint32_t SW128_DESC_HI = (uint32_t)(1024 >> 4) | 1u << 14 | 2u << 29;
-
-__device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t smem_addr, uint32_t leading_bytes) {
-    return ((smem_addr & 0x3FFFFu) >> 4) | (leading_bytes >> 4) << 16;
-}
-
-// D[tmem] (+)= A * B^T, kind::f16, operands by descriptor low words (A from
-// shared memory or, K-major by nature, from TMEM).
-__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
-                                          uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(SW128_DESC_HI), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
-                                          uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "mov.b64 db, {%2, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b_lo), "r"(SW128_DESC_HI), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-constexpr uint32_t IDESC_B_MN_MAJOR = 1u << 16;
 
 // Probabilities 2^(sc S - base) of one row's 128 scores at sb as bf16 pairs, and
 // their sum.  MASKED: columns from nv on count as -inf.

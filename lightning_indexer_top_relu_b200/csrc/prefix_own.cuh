@@ -18,8 +18,8 @@
 // than 2^8.  The streams merge in shared memory.
 #pragma once
 
+#include "cache_util.cuh"
 #include "common.cuh"
-#include "prefix_attn.cuh"
 #include "sparse_attn.cuh"
 
 namespace ic {
