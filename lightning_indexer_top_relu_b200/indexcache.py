@@ -9,6 +9,7 @@ non-zero status.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -223,6 +224,20 @@ def _raw_stream(stream, dev: int) -> Optional[int]:
     return _stream(stream)
 
 
+def _alloc_on(stream):
+    """Context in which a call's own allocations belong to the stream it
+    launches on: the caching allocator hands a freed workspace out again to
+    work ordered behind the call."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _new_ws(nbytes: int, device, stream) -> Optional[torch.Tensor]:
+    if not nbytes:
+        return None
+    with _alloc_on(stream):
+        return torch.empty(nbytes, device=device, dtype=torch.uint8)
+
+
 def _dev(t: torch.Tensor, name: str) -> int:
     """The current device's index; a leading operand elsewhere fails as in _ptr."""
     if t.get_device() < 0:
@@ -435,15 +450,16 @@ def prefix_attn(q, k_prefix, v_prefix, k=None, v=None, lens=None, scale: float =
             raise ValueError(f"k has {own_heads} heads, k_prefix has {Hkv}")
         _expect(v, tuple(k.shape), "v")
     _expect(lens, (B,), "lens")
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None and want_lse:
-        lse = torch.empty(B, Lq, Hq, device=q.device, dtype=torch.float32)
+    with _alloc_on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty(B, Lq, Hq, device=q.device, dtype=torch.float32)
     _expect(out, (B, Lq, Hq, d), "out")
     _expect(lse, (B, Lq, Hq), "lse")
     if ws is None:
         nbytes = prefix_attn_workspace_bytes(B, Lq, P, S, Hq, Hkv, d)
-        ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8) if nbytes else None
+        ws = _new_ws(nbytes, q.device, stream)
     dev, bf = _dev(q, "q"), torch.bfloat16
     rc = _lib.ic_prefix_attn(_at(q, dev, bf, "q"), _at(k_prefix, dev, bf, "k_prefix"),
                              _at(v_prefix, dev, bf, "v_prefix"), _at(k, dev, bf, "k"),
@@ -473,7 +489,7 @@ def attn_mass(q, k, lse, mass, lens=None, q_offset: int = 0, scale: float = 0.0,
     _expect(lens, (B,), "lens")
     if ws is None:
         nbytes = attn_mass_workspace_bytes(B, Lq, Lk, Hq, Hkv, d)
-        ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8) if nbytes else None
+        ws = _new_ws(nbytes, q.device, stream)
     dev, bf, f32 = _dev(q, "q"), torch.bfloat16, torch.float32
     rc = _lib.ic_attn_mass(_at(q, dev, bf, "q"), _at(k, dev, bf, "k"), _at(lse, dev, f32, "lse"),
                            _at(lens, dev, torch.int32, "lens"), B, Lq, Lk, Hq, Hkv, d, q_offset,
@@ -499,7 +515,7 @@ def attn_mass_sparse(q, k, idx, lse, mass, q_offset: int = 0, scale: float = 0.0
     _expect(mass, (B, Lk), "mass")
     if ws is None:
         nbytes = attn_mass_sparse_workspace_bytes(B, Lq, Lk)
-        ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8) if nbytes else None
+        ws = _new_ws(nbytes, q.device, stream)
     dev, bf, f32 = _dev(q, "q"), torch.bfloat16, torch.float32
     rc = _lib.ic_attn_mass_sparse(_at(q, dev, bf, "q"), _at(k, dev, bf, "k"),
                                   _at(idx, dev, torch.int32, "idx"), _at(lse, dev, f32, "lse"), B,
@@ -518,10 +534,11 @@ def evict_select(mass, n_keep: int, lens=None, n_sink: int = 0, n_recent: int = 
     (ic_evict_select)."""
     B, Lk = _dims_of(mass, 2, "mass")
     _expect(lens, (B,), "lens")
-    if keep is None:
-        keep = torch.empty(B, max(int(n_keep), 0), device=mass.device, dtype=torch.int32)
-    if new_lens is None:
-        new_lens = torch.empty(B, device=mass.device, dtype=torch.int32)
+    with _alloc_on(stream):
+        if keep is None:
+            keep = torch.empty(B, max(int(n_keep), 0), device=mass.device, dtype=torch.int32)
+        if new_lens is None:
+            new_lens = torch.empty(B, device=mass.device, dtype=torch.int32)
     _expect(keep, (B, n_keep), "keep")
     _expect(new_lens, (B,), "new_lens")
     dev, i32 = _dev(mass, "mass"), torch.int32

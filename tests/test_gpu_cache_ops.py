@@ -605,6 +605,47 @@ def test_two_streams_at_once(ic):
             assert torch.equal(x, y)
 
 
+def test_stream_argument_owns_the_calls_allocations(ic):
+    """A call on a stream that is not the current one takes its workspace
+    and outputs from that stream's memory: what the current stream allocates
+    and writes next leaves the call's results alone."""
+    g = gen(19)
+    B, P, S = 20, 9000, 300
+    q = randn(g, B, 1, 16, 128).bfloat16()
+    kp, vp = randn(g, P, 1, 128).bfloat16(), randn(g, P, 1, 128).bfloat16()
+    k, v = randn(g, B, S, 1, 128).bfloat16(), randn(g, B, S, 1, 128).bfloat16()
+    idx = torch.randint(0, P, (1, B, 64), generator=g, device="cuda", dtype=torch.int32).sort(-1).values
+    qs, ks = q.view(1, B, 16, 128), kp.view(1, P, 1, 128)
+
+    def step(stream):
+        out, lse = ic.prefix_attn(q, kp, vp, k, v, stream=stream)
+        rows = lse.view(1, B, 16)
+        dense = ic.attn_mass(qs, ks, rows, mass[0], q_offset=P, stream=stream)
+        sparse = ic.attn_mass_sparse(qs, ks, idx, rows, mass[1], q_offset=P - B, stream=stream)
+        return (out, lse, dense, sparse) + ic.evict_select(dense, P // 3, n_sink=4, stream=stream)
+
+    sizes = (ic.prefix_attn_workspace_bytes(B, 1, P, S, 16, 1, 128), ic.attn_mass_workspace_bytes(1, B, P, 16, 1, 128),
+             ic.attn_mass_sparse_workspace_bytes(1, B, P))
+    assert sizes[0] > 0 and sizes[2] > 0
+    mass = [torch.zeros(1, P, device="cuda") for _ in range(2)]
+    idx.clamp_(max=P - B)
+    want = [t.clone() for t in step(None)]
+    for m in mass:
+        m.zero_()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                 # the call's kernels wait behind this
+    got = step(side)
+    for n in sizes:                                   # the current stream goes on meanwhile
+        for _ in range(3):
+            torch.empty(max(n, 512), device="cuda", dtype=torch.uint8).fill_(255)
+    torch.cuda.synchronize()
+    ok(ic)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
 def test_offsets_past_32_bits(ic):
     """Caches of more than 2^31 elements (4.3 GB): rows at the far end are
     the ones attended, weighed, kept and moved."""
