@@ -53,11 +53,14 @@ MassGeom mass_geom(int B, int Lq, int Lk, int Hq, int Hkv, int d, int sms) {
     // few key tiles: several CTAs share one, with at least 8 steps each, as
     // long as they fill the GPU four times
     g.ranks = (int)std::max(1LL, std::min<long long>({32, g.row_tiles / 8, steps / 8, 4 * slots / tiles}));
-    // One row tile (decode): the keys stream past it, in one wave of CTAs (32
-    // caches of 32K: 40 us with 28 key tiles a CTA, 47 us with 10, 64 us with 2).
-    // More: CTAs of about 8 steps, as long as they fill the GPU four times.
-    long long group = steps == 1 ? (tiles + slots - 1) / slots
-                                 : g.ranks > 1 ? 1 : std::min((7 + steps) / steps, tiles / (4 * slots));
+    // One row tile a K/V head (decode): the keys stream past it, in one wave of
+    // CTAs (32 caches of 32K: 49 us with 29 key tiles a CTA, 67 us with 28, whose
+    // 320 CTAs take two waves; of ragged lengths 40 us with 29, 47 us with 10, 64 us
+    // with 2).  More: CTAs of about 8 steps, as long as they fill the GPU four times.
+    const long long per_seq = std::max(1LL, slots / B);
+    long long group = g.row_tiles == 1 && B <= slots ? (g.key_tiles + per_seq - 1) / per_seq
+                      : g.ranks > 1                  ? 1
+                                    : std::min((7 + steps) / steps, tiles / (4 * slots));
     group = std::max(group, (g.key_tiles + 65534LL) / 65535);
     g.group = (int)std::max(1LL, std::min<long long>(group, g.key_tiles));
     g.ws_bytes = g.ranks > 1 ? (size_t)g.ranks * B * Lk * sizeof(float) : 0;

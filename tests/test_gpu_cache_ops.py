@@ -204,6 +204,11 @@ MASS = [
     (1, 1, 100000, 16, 1, 64, False),
     (1, 20, 128, 128, 1, 128, False),
     (3, 9, 257, 5, 1, 128, True),
+    # several key tiles a CTA, of several K/V heads
+    (70, 2, 3000, 16, 4, 128, True),
+    (50, 1, 2500, 32, 8, 64, True),
+    (150, 3, 700, 8, 2, 64, True),
+    (300, 1, 300, 16, 1, 128, True),
 ]
 
 
