@@ -96,6 +96,7 @@ int check_prefix_sizes(int B, int Lq, int P, int S, int Hq) {
 // Work units of a shared-prefix attention and its partials per row.
 struct PrefixGeom {
     bool shared = false;
+    bool fused = false;            // units over the prefix and then their sequence's own cache, in the prefix fields
     int p_row_units = 0, p_splits = 0, p_tps = 0;
     int o_row_units = 0, o_splits = 0, o_tps = 0;
     int slots = 0;
@@ -109,7 +110,8 @@ struct PrefixGeom {
 // measured: 1.05 a step (one stream's 128 rows x 128 keys; 0.95 in a shared unit,
 // whose streams take turns and read half as much), 6 to start a unit and write
 // its partials, 8 for a shared one, which writes twice as many rows; 2 for
-// each 32 partials a row has to merge; an own tile as a unit counts two
+// each 32 partials a row has to merge, or their bytes at 4 TB/s where there are
+// many rows; an own tile as a unit counts two
 // steps.  Units up to the number of SMs run at once, more run in turn, the last
 // half a unit late on average.  The own-cache kernel reads 40 GB/s an SM (caches
 // taken as three quarters full), on SMs without a unit first.
@@ -141,6 +143,13 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
     const long long n_ou = (long long)B * g.o_row_units * Hkv;
     const double own_us = g.own_kernel ? 0.75 * B * S * Hkv * d * 4.0 / 40e3 : 0.0;   // of one SM
     double best = -1.0;
+    auto merge_us = [&](long long slots) {
+        return slots > 1 ? std::max(2.0 * ((slots + 31) / 32), (double)B * Lq * Hq * slots * (d + 1) * 4.0 / 4e6) : 0.0;
+    };
+    auto fewer_of = [](int nt, int tps) {                          // what one split more of nt tiles gives, if that is less
+        const int k = (nt + tps - 1) / tps + 1;
+        return std::min(tps - 1, (nt + k - 1) / k);
+    };
     for (int shared = 0; shared <= (rp > R ? 1 : 0); ++shared) {
         const int per_step = shared ? 2 : 1;
         const int row_units = has_p ? (int)((rp + R * per_step - 1) / (R * per_step)) : 0;
@@ -149,11 +158,7 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
         // tiles a split (own units, where this kernel has them, as many steps):
         // the values that some number of splits gives, about 2 sqrt(nt) of them
         const int nt = has_p ? p_nt : o_nt;
-        auto fewer = [&](int tps) {                                // what one split more gives, if that is less
-            const int k = (nt + tps - 1) / tps + 1;
-            return std::min(tps - 1, (nt + k - 1) / k);
-        };
-        for (int tps = nt; tps >= 1; tps = fewer(tps)) {
+        for (int tps = nt; tps >= 1; tps = fewer_of(nt, tps)) {
             const int p_tps = has_p ? tps : 0;
             const int steps = has_p ? p_tps * per_step : 2 * tps;
             const int o_tps = std::min(std::max(1, steps / 2), o_nt);
@@ -164,7 +169,7 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
             const double unit = ends + step_us * std::max(steps, has_o ? 2 * o_tps : 0);
             double est = n <= sms ? unit : std::max(unit, work / sms + 0.5 * unit);
             est += std::max(0.0, own_us - std::max(0.0, sms - n) * unit) / sms;
-            if (slots > 1) est += 2.0 * ((slots + 31) / 32);
+            est += merge_us(slots);
             if (n < 2147483647.0 && (best < 0.0 || est < best)) {
                 best = est;
                 g.shared = shared != 0;
@@ -175,6 +180,34 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
                 g.slots = (int)slots;
                 g.n_prefix = n_pu * p_sp;
                 g.n_own = n_ou * o_sp;
+            }
+        }
+    }
+    // Many rows a sequence: units over the prefix and the own cache together.  As
+    // measured: whole waves of units, 3 us to launch, 3 to start and end a unit (5 a
+    // shared one), 1.2 (d = 64: 1.0) or 1.9 a tile.  With as many own keys as
+    // queries half of the own tiles are above the diagonal.
+    const double diag = S > 0 ? 1.0 - 0.5 * std::min(Lq, S) / S : 1.0;
+    for (int shared = 0; has_o && S > 0 && P <= (1 << 30) - S && shared <= (ro > R ? 1 : 0); ++shared) {
+        const int per_step = shared ? 2 : 1, nt = p_nt + o_nt;
+        const long long row_units = (ro + R * per_step - 1) / (R * per_step), n_u = (long long)B * row_units * Hkv;
+        const double ends = shared ? 5.0 : 3.0, tile_us = shared ? 1.9 : d == 64 ? 1.0 : 1.2;
+        const double seen = (p_nt + diag * o_nt) / nt;
+        for (int tps = nt; tps >= 1; tps = fewer_of(nt, tps)) {
+            const int splits = (nt + tps - 1) / tps;
+            const double n = (double)n_u * splits, unit = ends + tile_us * tps;
+            const double mean = n <= 2.0 * sms ? unit : ends + tile_us * tps * seen;   // few waves: the longest units count
+            const double est = 3.0 + std::max(unit, std::ceil(n / sms) * mean) + merge_us(splits);
+            if (n < 2147483647.0 && est < best) {
+                best = est;
+                g.fused = true;
+                g.shared = shared != 0;
+                g.p_row_units = (int)row_units;
+                g.p_tps = tps;
+                g.p_splits = g.slots = splits;
+                g.o_row_units = g.o_splits = g.o_tps = 0;
+                g.n_prefix = (long long)n;
+                g.n_own = 0;
             }
         }
     }
@@ -328,10 +361,10 @@ int ic_prefix_attn(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* 
     const unsigned grid = (unsigned)(g.n_prefix + g.n_own);
     a.to_parts = g.slots > 1 ? 1 : 0;
     if (grid > 0) {
-        if (d == 64)
-            ic::prefix_attn_kernel<64><<<grid, ic::PA_THREADS, ic::PrefixSmem<64>::ALLOC, st>>>(tkp, tvp, tk, tv, a);
-        else
-            ic::prefix_attn_kernel<128><<<grid, ic::PA_THREADS, ic::PrefixSmem<128>::ALLOC, st>>>(tkp, tvp, tk, tv, a);
+        auto* kernel = d == 64 ? (g.fused ? ic::prefix_attn_kernel<64, true> : ic::prefix_attn_kernel<64, false>)
+                               : (g.fused ? ic::prefix_attn_kernel<128, true> : ic::prefix_attn_kernel<128, false>);
+        kernel<<<grid, ic::PA_THREADS, d == 64 ? ic::PrefixSmem<64>::ALLOC : ic::PrefixSmem<128>::ALLOC, st>>>(
+            tkp, tvp, tk, tv, a);
         if (launched(cudaGetLastError(), "prefix_attn launch")) return IC_ERR_CUDA;
     }
     if (g.own_kernel && (rc = launch_prefix_own(g, a, k, v, d, grid > 0, st))) return rc;

@@ -396,8 +396,10 @@ bool evict_cluster_fits_all(int c) {
 }
 
 template <int D>
-void set_own_attr() {
+void set_prefix_attr() {
     const auto max = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaFuncSetAttribute(ic::prefix_attn_kernel<D, false>, max, ic::PrefixSmem<D>::ALLOC);
+    cudaFuncSetAttribute(ic::prefix_attn_kernel<D, true>, max, ic::PrefixSmem<D>::ALLOC);
     cudaFuncSetAttribute(ic::prefix_own_kernel<D, 1>, max, ic::OwnSmem<D>::BYTES);
     cudaFuncSetAttribute(ic::prefix_own_kernel<D, 2>, max, ic::OwnSmem<D>::BYTES);
     cudaFuncSetAttribute(ic::prefix_own_kernel<D, 4>, max, ic::OwnSmem<D>::BYTES);
@@ -839,12 +841,8 @@ int device_setup(int* dev_out, int* sms_out) {
                              cudaFuncAttributeMaxDynamicSharedMemorySize, ic::SaSmem<64>::BYTES);
         cudaFuncSetAttribute(ic::sparse_attn_kernel<128>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, ic::SaSmem<128>::BYTES);
-        cudaFuncSetAttribute(ic::prefix_attn_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             ic::PrefixSmem<64>::ALLOC);
-        cudaFuncSetAttribute(ic::prefix_attn_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             ic::PrefixSmem<128>::ALLOC);
-        set_own_attr<64>();
-        set_own_attr<128>();
+        set_prefix_attr<64>();
+        set_prefix_attr<128>();
         cudaFuncSetAttribute(ic::attn_mass_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ic::AM_SMEM);
         cudaFuncSetAttribute(ic::attn_mass_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -97,6 +97,15 @@ PREFIX = [
     (1, 2, 40, 20000, 8, 2, 64),     # long own cache
     (70, 1, 20, 3, 128, 1, 128),     # 128 heads
     (300, 1, 2500, 17, 16, 1, 64),
+    # many rows a sequence: the prefix's tiles, then the own cache's
+    (2, 64, 300, 700, 16, 1, 128),
+    (3, 40, 129, 257, 16, 2, 64),
+    (2, 33, 0, 500, 8, 1, 128),      # no prefix
+    (1, 130, 1000, 130, 4, 4, 64),
+    (6, 9, 2000, 50, 16, 1, 128),
+    (150, 9, 256, 100, 16, 1, 128),  # more units than fit at once
+    (5, 20, 1, 129, 13, 1, 64),
+    (4, 300, 5, 40, 8, 2, 128),      # more queries than own keys
 ]
 
 
