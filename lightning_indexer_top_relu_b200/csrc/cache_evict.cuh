@@ -256,22 +256,23 @@ struct GatherArgs {
 template <typename V>
 __device__ __forceinline__ void cg_copy(const uint8_t* src, uint8_t* dst, long long row_bytes,
                                         const int* rows, int nr) {
-    const long long cpr = row_bytes / (long long)sizeof(V);
-    const long long total = cpr * nr;
-    for (long long e0 = threadIdx.x; e0 < total; e0 += 4 * CG_THREADS) {
+    const uint32_t cpr = (uint32_t)(row_bytes / (long long)sizeof(V));
+    const uint32_t total = cpr * (uint32_t)nr;                   // < 2^32: rows of at most 2^22 chunks
+    for (uint32_t e0 = threadIdx.x; e0 < total; e0 += 4 * CG_THREADS) {
         V v[4];
-        long long at[4];
+        bool put[4];
+        // unconditional loads (an empty slot's from row 0, past the end the last
+        // chunk again), so that all four are under way at once
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const long long e = e0 + u * CG_THREADS;
-            const int r = (int)(e / cpr);
-            const int id = e < total ? rows[r] : -1;
-            at[u] = id >= 0 ? e : -1;
-            if (id >= 0) v[u] = __ldg(reinterpret_cast<const V*>(src + id * row_bytes) + (e - r * cpr));
+            const uint32_t e = min(e0 + u * CG_THREADS, total - 1), r = e / cpr;
+            const int id = rows[r];
+            put[u] = id >= 0 && e0 + u * CG_THREADS < total;
+            v[u] = __ldg(reinterpret_cast<const V*>(src + max(id, 0) * row_bytes) + (e - r * cpr));
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (at[u] >= 0) reinterpret_cast<V*>(dst)[at[u]] = v[u];
+            if (put[u]) reinterpret_cast<V*>(dst)[e0 + u * CG_THREADS] = v[u];
     }
 }
 
