@@ -50,9 +50,12 @@ MassGeom mass_geom(int B, int Lq, int Lk, int Hq, int Hkv, int d, int sms) {
     const long long tiles = (long long)B * g.key_tiles;
     const long long steps = (long long)g.row_tiles * Hkv;          // of a key tile that every row sees
     const long long slots = 2LL * sms;                             // CTAs at once
-    // few key tiles: several CTAs share one, with at least 8 steps each, as
-    // long as they fill the GPU four times
-    g.ranks = (int)std::max(1LL, std::min<long long>({32, g.row_tiles / 8, steps / 8, 4 * slots / tiles}));
+    // few key tiles: several CTAs share one, with at least 8 steps each, as long as
+    // they fill the GPU four times; with at least 4 as long as all of them run
+    // at once (200 rows, two K/V heads, 3000 keys: 14 us instead of 32)
+    const long long deep = std::min<long long>({g.row_tiles / 8, steps / 8, 4 * slots / tiles});
+    const long long wide = std::min<long long>({(long long)g.row_tiles, steps / 4, slots / tiles});
+    g.ranks = (int)std::max(1LL, std::min(32LL, std::max(deep, wide)));
     // One row tile a K/V head (decode): the keys stream past it, in one wave of
     // CTAs (32 caches of 32K: 49 us with 29 key tiles a CTA, 67 us with 28, whose
     // 320 CTAs take two waves; of ragged lengths 40 us with 29, 47 us with 10, 64 us
