@@ -126,6 +126,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                  const AttnMassArgs a) {
     using S = MassSmem<D>;
     extern __shared__ uint8_t am_raw[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the adding kernel may take SMs as they come free
     const int warp = warp_uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int rank = blockIdx.x, C = gridDim.x, b = blockIdx.z;
     const int n = warp_uniform(seq_len(a.lens, b, a.Lk));
@@ -372,6 +373,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 
 // mass += the ranks' sums, in rank order.
 __global__ void attn_mass_add_kernel(const AttnMassArgs a, int ranks) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");          // launched as the sums' dependent
     const int b = blockIdx.y;
     const int n = seq_len(a.lens, b, a.Lk);
     for (long long s = (long long)blockIdx.x * blockDim.x + threadIdx.x; s < n; s += (long long)gridDim.x * blockDim.x) {
@@ -414,6 +416,7 @@ template <int D>
 __global__ void __launch_bounds__(128, 4)
 attn_mass_sparse_kernel(const SparseMassArgs a) {
     constexpr int NJ = D / 32;                                  // 16-byte chunks a lane and row
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const long long row = blockIdx.x;
@@ -492,8 +495,8 @@ attn_mass_sparse_kernel(const SparseMassArgs a) {
     }
 }
 
-__global__ void mass_add_fixed_kernel(float* __restrict__ mass, const unsigned long long* __restrict__ acc,
-                                      long long n, double unit) {
+__global__ void mass_add_fixed_kernel(float* mass, const unsigned long long* acc, long long n, double unit) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");          // launched as the sums' dependent
     for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n;
          e += (long long)gridDim.x * blockDim.x) {
         const unsigned long long v = acc[e];

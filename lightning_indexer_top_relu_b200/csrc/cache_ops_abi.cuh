@@ -242,10 +242,10 @@ int make_tmap(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, 
 // Launches `kernel`; with `dependent` as the programmatic dependent of the
 // kernel before it on the stream, whose results it waits for itself.
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, bool dependent,
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem, bool dependent,
                              cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -440,8 +440,8 @@ int ic_attn_mass(const uint16_t* q, const uint16_t* k, const float* lse, const i
     if (launched(cudaGetLastError(), "attn_mass launch")) return IC_ERR_CUDA;
     if (g.ranks == 1) return IC_OK;
     const dim3 ag((unsigned)std::min(Lk / 256 + 1, 4 * sms), (unsigned)B);
-    ic::attn_mass_add_kernel<<<ag, 256, 0, st>>>(a, g.ranks);
-    return launched(cudaGetLastError(), "attn_mass add launch");
+    return launched(launch_dependent(ic::attn_mass_add_kernel, ag, 256, 0, true, st, a, g.ranks),
+                    "attn_mass add launch");
 }
 
 size_t ic_attn_mass_sparse_workspace_bytes(int B, int Lq, int Lk) {
@@ -500,9 +500,10 @@ int ic_attn_mass_sparse(const uint16_t* q, const uint16_t* k, const int32_t* idx
     if (launched(cudaGetLastError(), "attn_mass_sparse launch")) return IC_ERR_CUDA;
     if (need == 0) return IC_OK;
     const long long n = (long long)B * Lk;
-    ic::mass_add_fixed_kernel<<<(unsigned)std::min<long long>((n + 255) / 256, 8LL * sms), 256, 0, st>>>(
-        mass, a.acc, n, std::ldexp(1.0, -shift));
-    return launched(cudaGetLastError(), "mass_add_fixed launch");
+    const unsigned ag = (unsigned)std::min<long long>((n + 255) / 256, 8LL * sms);
+    return launched(launch_dependent(ic::mass_add_fixed_kernel, ag, 256, 0, true, st, mass, a.acc, n,
+                                     std::ldexp(1.0, -shift)),
+                    "mass_add_fixed launch");
 }
 
 int ic_evict_select(const float* mass, const int32_t* lens, int B, int Lk, int n_keep, int n_sink,
