@@ -389,8 +389,10 @@ EVICT = [
     (2, 20000, 3001, 5, 0, "special"),    # NaN, infinities, zeros of both signs
     (70, 3000, 1500, 4, 128, "random"),
     (2, 40000, 30011, 16, 999, "random"),
-    (1, 400001, 50001, 3, 17, "ties"),    # slices longer than shared memory
+    (1, 400001, 50001, 3, 17, "ties"),
     (1, 400001, 70000, 0, 0, "random"),
+    (1, 700001, 50001, 3, 17, "ties"),    # slices longer than shared memory
+    (2, 900000, 450000, 0, 0, "special"),
 ]
 
 
