@@ -449,7 +449,8 @@ size_t ic_attn_mass_sparse_workspace_bytes(int B, int Lq, int Lk);
  * -INFINITY).  Positions are written ascending, then -1.  new_lens[b] =
  * min(n, n_keep).  n_sink + n_recent <= n_keep.  A length outside [0, Lk] is
  * clamped and flags IC_ERR_INVALID_ARG in the device error word.  B <= 65535,
- * Lk and n_keep <= 2^30.  Exact.
+ * Lk and n_keep <= 2^30.  new_lens may be lens (lengths updated in place); keep
+ * and new_lens otherwise overlap nothing of the call (IC_ERR_INVALID_ARG).  Exact.
  */
 int ic_evict_select(const float *mass, const int32_t *lens, int B, int Lk, int n_keep, int n_sink,
                     int n_recent, int32_t *keep, int32_t *new_lens, ic_stream_t stream);

@@ -41,7 +41,7 @@ struct EvictArgs {
     const float* mass;       // [B, Lk]
     const int32_t* lens;     // [B] or null
     int32_t* keep;           // [B, n_keep]
-    int32_t* new_lens;       // [B] or null
+    int32_t* new_lens;       // [B] or null; may be lens itself
     int B, Lk, n_keep, n_sink, n_recent;
     int cached;              // slices fit in shared memory
 };
@@ -115,10 +115,14 @@ evict_select_kernel(const EvictArgs a) {
     uint32_t* keys = reinterpret_cast<uint32_t*>(ev_smem + S::OFF_KEYS);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x, C = gridDim.x, b = blockIdx.y;      // the cluster is one row of the grid
-    const int n = seq_len(a.lens, b, a.Lk);
+    // new_lens may be lens, so the length is a plain load, once a thread, and
+    // the new one is written where no thread of the cluster can take it for
+    // the old: here when every position stays (the clamped length itself,
+    // which clamps to the same n), else behind the barriers of the passes
+    const int n = a.lens ? clamp_len(*(const volatile int32_t*)(a.lens + b), a.Lk) : a.Lk;
     int32_t* keep = a.keep + (long long)b * a.n_keep;
-    if (rank == 0 && tid == 0 && a.new_lens) a.new_lens[b] = min(n, a.n_keep);
     if (n <= a.n_keep) {                                             // uniform over the cluster
+        if (rank == 0 && tid == 0 && a.new_lens) a.new_lens[b] = n;
         for (int j = rank * NT + tid; j < a.n_keep; j += C * NT) keep[j] = j < n ? j : -1;
         return;
     }
@@ -195,6 +199,7 @@ evict_select_kernel(const EvictArgs a) {
         }
         __syncthreads();
     }
+    if (rank == 0 && tid == 0 && a.new_lens) a.new_lens[b] = a.n_keep;
     const uint32_t T = kk > 0 ? prefix : 0xffffffffu;    // no weight's key is 0xffffffff
     const int need = remaining;                          // keys equal to T kept, lowest positions first
 

@@ -19,10 +19,32 @@ float scale_log2_of(float scale, int d) {
 // Most CTAs one launch may have in its first grid dimension.
 constexpr long long MAX_GRID_X = 2147483647LL;
 
-// Bytes [a, a + na) and [b, b + nb) share some.
+// Bytes [a, a + na) and [b, b + nb) share some (a null or empty buffer none).
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    if (!a || !b || na == 0 || nb == 0) return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + nb && y < x + na;
+}
+
+// One buffer of a call.
+struct Span {
+    const char* name;
+    const void* p;
+    size_t n;
+};
+
+// What a call writes overlaps neither what it reads nor what else it writes:
+// its CTAs read and write in no order.
+int check_disjoint(std::initializer_list<Span> writes, std::initializer_list<Span> reads) {
+    for (const Span* w = writes.begin(); w != writes.end(); ++w) {
+        for (const Span& r : reads)
+            if (overlap(w->p, w->n, r.p, r.n))
+                return fail(IC_ERR_INVALID_ARG, "%s overlaps %s", w->name, r.name);
+        for (const Span* o = writes.begin(); o != w; ++o)
+            if (overlap(w->p, w->n, o->p, o->n))
+                return fail(IC_ERR_INVALID_ARG, "%s overlaps %s", w->name, o->name);
+    }
+    return IC_OK;
 }
 
 // Sizes whose positions the kernels count in 32 bits.
@@ -521,9 +543,14 @@ int ic_evict_select(const float* mass, const int32_t* lens, int B, int Lk, int n
     if (B > 65535 || Lk > (1 << 30) || n_keep > (1 << 30))
         return fail(IC_ERR_UNSUPPORTED, "B=%d Lk=%d n_keep=%d (supported: B <= 65535, Lk and n_keep <= 2^30)", B,
                     Lk, n_keep);
-    int dev, sms;
-    int rc = device_setup(&dev, &sms);
+    // lengths may be updated in place
+    const size_t nl = (size_t)B * 4;
+    const Span m{"mass", mass, nl * Lk}, l{"lens", lens, nl};
+    const Span kp{"keep", keep, nl * n_keep}, nw{"new_lens", new_lens, nl};
+    int rc = new_lens != lens ? check_disjoint({kp, nw}, {m, l}) : check_disjoint({kp, nw}, {m});
     if (rc) return rc;
+    int dev, sms;
+    if ((rc = device_setup(&dev, &sms))) return rc;
     ic::EvictArgs a{};
     a.mass = mass;
     a.lens = lens;

@@ -10,16 +10,18 @@ namespace ic {
 // A further bit of the device error word.
 constexpr unsigned DEV_ERR_BAD_LENGTH = 8u;   // a sequence length outside [0, capacity] (clamped)
 
-// Positions of its own cache that sequence b holds; a length outside [0, cap]
-// is clamped and reported.
-__device__ __forceinline__ int seq_len(const int32_t* lens, int b, int cap) {
-    if (lens == nullptr) return cap;
-    const int n = __ldg(lens + b);
+// A length outside [0, cap] is clamped and reported.
+__device__ __forceinline__ int clamp_len(int n, int cap) {
     if (n < 0 || n > cap) {
         report(DEV_ERR_BAD_LENGTH);
         return n < 0 ? 0 : cap;
     }
     return n;
+}
+
+// Positions of its own cache that sequence b holds.
+__device__ __forceinline__ int seq_len(const int32_t* lens, int b, int cap) {
+    return lens == nullptr ? cap : clamp_len(__ldg(lens + b), cap);
 }
 
 // ---------------------------------------------------------------- barriers, warps, clusters

@@ -531,7 +531,7 @@ def evict_select(mass, n_keep: int, lens=None, n_sink: int = 0, n_recent: int = 
     """(keep [B,n_keep] int32, new_lens [B] int32): the ascending positions
     each cache keeps under a budget of n_keep -- the first n_sink, the last
     n_recent and the others of most mass [B,Lk] fp32 -- padded with -1
-    (ic_evict_select)."""
+    (ic_evict_select).  new_lens=lens updates the lengths in place."""
     B, Lk = _dims_of(mass, 2, "mass")
     _expect(lens, (B,), "lens")
     with _alloc_on(stream):

@@ -1,0 +1,52 @@
+"""Calls of the KV-cache entry points whose buffers coincide where that is
+allowed, on the GPU."""
+import pytest
+import torch
+
+from lightning_indexer_top_relu_b200 import build
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ic():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    build.build()
+    from lightning_indexer_top_relu_b200 import indexcache
+    return indexcache
+
+
+# caches in one CTA, in clusters of 2 and of more, with slices past shared memory
+@pytest.mark.parametrize("B,Lk,n_keep", [(1, 50, 20), (5, 3000, 700), (40, 6000, 100), (3, 50000, 20000),
+                                         (1, 700001, 5000), (200, 9000, 4000)])
+def test_evict_select_updates_lengths_in_place(ic, B, Lk, n_keep):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B + Lk)
+    mass = torch.rand(B, Lk, device="cuda", generator=g)
+    lens = torch.randint(0, Lk + 1, (B,), device="cuda", generator=g, dtype=torch.int32)
+    lens[0] = Lk
+    lens[B // 2] = min(n_keep + 1, Lk)
+    if B > 3:
+        lens[1], lens[3] = n_keep, 0
+    before = lens.clone()
+    keep, new_lens = ic.evict_select(mass, n_keep, lens=lens, n_sink=4, n_recent=9)
+    torch.cuda.synchronize()
+    assert ic.get_last_device_error() == 0 and torch.equal(lens, before)
+    for _ in range(20):
+        lens.copy_(before)
+        again, same = ic.evict_select(mass, n_keep, lens=lens, n_sink=4, n_recent=9, new_lens=lens)
+        torch.cuda.synchronize()
+        assert ic.get_last_device_error() == 0
+        assert same is lens and torch.equal(lens, new_lens) and torch.equal(again, keep)
+    # lengths outside [0, Lk] are clamped and flagged in place too
+    lens.copy_(before)
+    lens[0] = Lk + 7
+    lens[-1] = -2 if B > 1 else Lk + 7
+    keep, new_lens = ic.evict_select(mass, n_keep, lens=lens.clone())
+    torch.cuda.synchronize()
+    assert ic.get_last_device_error() == 1
+    again, _ = ic.evict_select(mass, n_keep, lens=lens, new_lens=lens)
+    torch.cuda.synchronize()
+    assert ic.get_last_device_error() == 1
+    assert torch.equal(lens, new_lens) and torch.equal(again, keep)
