@@ -379,7 +379,9 @@ int ic_index_overlap(const int32_t *idx_a, const int32_t *idx_b, long long n_row
  * IC_ERR_INVALID_ARG in the device error word.  d in {64, 128}; Hq <= 128 a
  * multiple of Hkv, query head h reads K/V head h / (Hq / Hkv).  scale <= 0
  * selects 1/sqrt(d).
- * lens is not read when S == 0 and P > 0.  P and S up to 2^30.
+ * lens is not read when S == 0 and P > 0.  P and S up to 2^30.  out, lse and
+ * the workspace overlap nothing else of the call (IC_ERR_INVALID_ARG): no
+ * attention in place over q.
  * ws/ws_bytes: device workspace of ic_prefix_attn_workspace_bytes(...) bytes
  * for the partial results of rows whose keys are split over several CTAs (may
  * be NULL when that is 0); less returns IC_ERR_WORKSPACE_TOO_SMALL.

@@ -345,11 +345,18 @@ int ic_prefix_attn(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* 
     if (ws_bytes > 0 && !ws) return fail(IC_ERR_INVALID_ARG, "ws is NULL but ws_bytes > 0");
     if (ws && !aligned16(ws)) return fail(IC_ERR_UNSUPPORTED, "ws must be 16-byte aligned");
     if ((rc = check_prefix_sizes(B, Lq, P, S, Hq))) return rc;
+    // several CTAs read a row's query, and their partials meet in a later kernel
+    const size_t nq = (size_t)B * Lq * Hq, kv_row = (size_t)Hkv * d * 2;
+    const Span o{"out", out, nq * d * 2}, ls{"lse", lse, nq * 4}, qs{"q", q, nq * d * 2};
+    const Span kps{"k_prefix", k_prefix, P * kv_row}, vps{"v_prefix", v_prefix, P * kv_row};
+    const Span ks{"k", k, (size_t)B * S * kv_row}, vs{"v", v, (size_t)B * S * kv_row}, ns{"lens", lens, (size_t)B * 4};
+    if ((rc = check_disjoint({o, ls}, {qs, kps, vps, ks, vs, ns}))) return rc;
     int dev, sms;
     if ((rc = device_setup(&dev, &sms))) return rc;
     const PrefixGeom g = prefix_geom(B, Lq, P, S, Hq, Hkv, d, sms);
     if (ws_bytes < g.ws_bytes)
         return fail(IC_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", ws_bytes, g.ws_bytes);
+    if ((rc = check_disjoint({{"ws", ws, g.ws_bytes}}, {o, ls, qs, kps, vps, ks, vs, ns}))) return rc;
     CUtensorMap tkp{}, tvp{}, tk{}, tv{};
     const uint64_t hd = (uint64_t)Hkv * d;
     if (P > 0) {

@@ -432,7 +432,7 @@ def prefix_attn(q, k_prefix, v_prefix, k=None, v=None, lens=None, scale: float =
     keys k_prefix, v_prefix [P,Hkv,d] (or [P,d]): row i of sequence b also
     sees its own cache k, v [B,S,Hkv,d] (or [B,S,d]; None: no own cache) up to
     position lens[b] - Lq + i (lens [B] int32; None: S everywhere).  ws=None
-    allocates the workspace (prefix_attn_workspace_bytes)."""
+    allocates the workspace (prefix_attn_workspace_bytes).  out may not be q."""
     B, Lq, Hq, d = _dims_of(q, 4, "q")
     if k_prefix.dim() == 3:
         P, Hkv = k_prefix.shape[0], k_prefix.shape[1]

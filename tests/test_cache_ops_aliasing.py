@@ -41,3 +41,26 @@ def test_evict_select(ic):
     assert overlaps(ic, call(new=0x200004), "new_lens", "lens")
     assert overlaps(ic, call(new=0x200000, lens=0x200008), "new_lens", "lens")
     assert overlaps(ic, call(new=0x200000, keep=0x200000), "new_lens", "keep")
+
+
+def test_prefix_attn(ic):
+    at = dict(q=0x1000000, kp=0x2000000, vp=0x3000000, k=0x4000000, v=0x5000000, lens=0x6000000,
+              out=0x7000000, lse=0x8000000)
+    # q and out 2 * 3 * 8 * 64 * 2 = 0x1800 bytes, lse 0xc0, a prefix tensor 70 * 2 * 64 * 2 = 0x4600,
+    # an own one 2 * 50 * 256 = 0x6400, lens 8
+
+    def call(**kw):
+        a = dict(at, **kw)
+        return ic.lib().ic_prefix_attn(a["q"], a["kp"], a["vp"], a["k"], a["v"], a["lens"], 2, 3, 70, 50, 8, 2, 64,
+                                       0.0, a["out"], a["lse"], None, 0, None)
+    assert overlaps(ic, call(out=at["q"]), "out", "q")
+    assert overlaps(ic, call(out=at["q"] + 0x1780), "out", "q")
+    assert overlaps(ic, call(out=at["q"] - 0x1780), "out", "q")
+    assert overlaps(ic, call(out=at["kp"] + 0x45f0), "out", "k_prefix")
+    assert overlaps(ic, call(out=at["vp"]), "out", "v_prefix")
+    assert overlaps(ic, call(out=at["k"] + 0x63f0), "out", "k")
+    assert overlaps(ic, call(out=at["v"]), "out", "v")
+    assert overlaps(ic, call(out=at["lens"]), "out", "lens")
+    assert overlaps(ic, call(lse=at["q"] + 0x17fc), "lse", "q")
+    assert overlaps(ic, call(lse=at["out"]), "lse", "out")
+    assert overlaps(ic, call(lse=at["lens"] + 4), "lse", "lens")

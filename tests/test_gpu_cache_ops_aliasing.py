@@ -50,3 +50,33 @@ def test_evict_select_updates_lengths_in_place(ic, B, Lk, n_keep):
     torch.cuda.synchronize()
     assert ic.get_last_device_error() == 1
     assert torch.equal(lens, new_lens) and torch.equal(again, keep)
+
+
+def test_prefix_attn_refuses_outputs_over_its_operands(ic):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+
+    def randn(*shape):
+        return torch.randn(*shape, device="cuda", generator=g).bfloat16()
+    B, P, S, d = 20, 3000, 100, 128
+    q, kp, vp = randn(B, 1, 16, d), randn(P, 1, d), randn(P, 1, d)
+    k, v = randn(B, S, 1, d), randn(B, S, 1, d)
+    lens = torch.full((B,), S, device="cuda", dtype=torch.int32)
+    n = ic.prefix_attn_workspace_bytes(B, 1, P, S, 16, 1, d)
+    # one arena: the workspace, then the queries where it ends
+    arena = torch.zeros(n + q.numel() * 2, device="cuda", dtype=torch.uint8)
+    assert n > 0 and n % 16 == 0
+    tail = arena[n:].view(torch.bfloat16).view_as(q)
+    tail.copy_(q)
+    want = ic.prefix_attn(q, kp, vp, k, v, lens)
+    got = ic.prefix_attn(tail, kp, vp, k, v, lens, ws=arena)        # only the bytes needed count
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(ic.IndexCacheError, match="out overlaps q"):
+        ic.prefix_attn(q, kp, vp, k, v, lens, out=q)
+    with pytest.raises(ic.IndexCacheError, match="ws overlaps q"):
+        ic.prefix_attn(arena[n - 16:-16].view(torch.bfloat16).view_as(q), kp, vp, k, v, lens, ws=arena)
+    with pytest.raises(ic.IndexCacheError, match="ws overlaps k"):
+        ic.prefix_attn(q, kp, vp, arena[:k.numel() * 2].view(torch.bfloat16).view_as(k), v, lens, ws=arena)
+    torch.cuda.synchronize()
+    assert torch.equal(tail, q) and ic.get_last_device_error() == 0
