@@ -412,7 +412,8 @@ size_t ic_prefix_attn_workspace_bytes(int B, int Lq, int P, int S, int Hq, int H
  * the same bits.
  * ws/ws_bytes: device workspace of ic_attn_mass_workspace_bytes(...) bytes for
  * the sums of rows that several CTAs share (may be NULL when that is 0); less
- * returns IC_ERR_WORKSPACE_TOO_SMALL.
+ * returns IC_ERR_WORKSPACE_TOO_SMALL.  mass and the workspace overlap nothing
+ * else of the call (IC_ERR_INVALID_ARG; also of ic_attn_mass_sparse).
  */
 int ic_attn_mass(const uint16_t *q, const uint16_t *k, const float *lse, const int32_t *lens, int B,
                  int Lq, int Lk, int Hq, int Hkv, int d, int q_offset, float scale, float *mass,

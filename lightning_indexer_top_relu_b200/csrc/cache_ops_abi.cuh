@@ -433,11 +433,16 @@ int ic_attn_mass(const uint16_t* q, const uint16_t* k, const float* lse, const i
     if (ws_bytes > 0 && !ws) return fail(IC_ERR_INVALID_ARG, "ws is NULL but ws_bytes > 0");
     if (ws && !aligned16(ws)) return fail(IC_ERR_UNSUPPORTED, "ws must be 16-byte aligned");
     if ((rc = check_mass_sizes(B, Lq, Lk))) return rc;
+    const size_t nq = (size_t)B * Lq * Hq, nk = (size_t)B * Lk;
+    const Span ms{"mass", mass, nk * 4}, qs{"q", q, nq * d * 2}, ks{"k", k, nk * Hkv * d * 2};
+    const Span ls{"lse", lse, nq * 4}, ns{"lens", lens, (size_t)B * 4};
+    if ((rc = check_disjoint({ms}, {qs, ks, ls, ns}))) return rc;
     int dev, sms;
     if ((rc = device_setup(&dev, &sms))) return rc;
     const MassGeom g = mass_geom(B, Lq, Lk, Hq, Hkv, d, sms);
     if (ws_bytes < g.ws_bytes)
         return fail(IC_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", ws_bytes, g.ws_bytes);
+    if ((rc = check_disjoint({{"ws", ws, g.ws_bytes}}, {ms, qs, ks, ls, ns}))) return rc;
     CUtensorMap tq, tk;
     const uint64_t hd = (uint64_t)Hkv * d, qd = (uint64_t)Hq * d;
     {
@@ -499,6 +504,11 @@ int ic_attn_mass_sparse(const uint16_t* q, const uint16_t* k, const int32_t* idx
                     ws ? ws_bytes : (size_t)0, need);
     const long long rows = (long long)B * Lq;
     if (rows > MAX_GRID_X) return fail(IC_ERR_UNSUPPORTED, "B*Lq = %lld too large", rows);
+    const size_t nk = (size_t)B * Lk;
+    if ((rc = check_disjoint({{"mass", mass, nk * 4}, {"ws", ws, need}},
+                             {{"q", q, (size_t)rows * Hq * d * 2}, {"k", k, nk * d * 2},
+                              {"idx", idx, (size_t)rows * k_slots * 4}, {"lse", lse, (size_t)rows * Hq * 4}})))
+        return rc;
     int dev, sms;
     if ((rc = device_setup(&dev, &sms))) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

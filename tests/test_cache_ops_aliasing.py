@@ -64,3 +64,37 @@ def test_prefix_attn(ic):
     assert overlaps(ic, call(lse=at["q"] + 0x17fc), "lse", "q")
     assert overlaps(ic, call(lse=at["out"]), "lse", "out")
     assert overlaps(ic, call(lse=at["lens"] + 4), "lse", "lens")
+
+
+def test_attn_mass(ic):
+    at = dict(q=0x1000000, k=0x2000000, lse=0x3000000, lens=0x4000000, mass=0x5000000)
+    # q 2 * 3 * 8 * 64 * 2 = 0x1800 bytes, k 2 * 50 * 2 * 64 * 2 = 0x6400, lse 0xc0, mass 400
+
+    def call(**kw):
+        a = dict(at, **kw)
+        return ic.lib().ic_attn_mass(a["q"], a["k"], a["lse"], a["lens"], 2, 3, 50, 8, 2, 64, 0, 0.0, a["mass"],
+                                     None, 0, None)
+    assert overlaps(ic, call(mass=at["q"] + 0x17fc), "mass", "q")
+    assert overlaps(ic, call(mass=at["k"] - 396), "mass", "k")
+    assert overlaps(ic, call(mass=at["k"] + 0x63fc), "mass", "k")
+    assert overlaps(ic, call(mass=at["lse"]), "mass", "lse")
+    assert overlaps(ic, call(mass=at["lens"] + 4), "mass", "lens")
+
+
+def test_attn_mass_sparse(ic):
+    at = dict(q=0x1000000, k=0x2000000, idx=0x3000000, lse=0x4000000, mass=0x5000000, ws=0x6000000)
+    # q 0x1800 bytes, k 2 * 50 * 64 * 2 = 0x3200, idx 2 * 3 * 10 * 4 = 240, lse 0xc0, mass 400, ws 800
+
+    def call(**kw):
+        a = dict(at, **kw)
+        return ic.lib().ic_attn_mass_sparse(a["q"], a["k"], a["idx"], a["lse"], 2, 3, 50, 8, 1, 64, 10, 40, 0.0,
+                                            a["mass"], a["ws"], 1 << 12, None)
+    assert overlaps(ic, call(mass=at["q"]), "mass", "q")
+    assert overlaps(ic, call(mass=at["k"] + 0x31fc), "mass", "k")
+    assert overlaps(ic, call(mass=at["idx"] + 236), "mass", "idx")
+    assert overlaps(ic, call(mass=at["lse"] - 396), "mass", "lse")
+    assert overlaps(ic, call(ws=at["mass"] - 784), "ws", "mass")
+    assert overlaps(ic, call(ws=at["idx"] + 0xe0), "ws", "idx")
+    assert overlaps(ic, call(ws=at["q"] - 784), "ws", "q")
+    assert overlaps(ic, call(ws=at["k"]), "ws", "k")
+    assert overlaps(ic, call(ws=at["lse"]), "ws", "lse")

@@ -80,3 +80,21 @@ def test_prefix_attn_refuses_outputs_over_its_operands(ic):
         ic.prefix_attn(q, kp, vp, arena[:k.numel() * 2].view(torch.bfloat16).view_as(k), v, lens, ws=arena)
     torch.cuda.synchronize()
     assert torch.equal(tail, q) and ic.get_last_device_error() == 0
+
+
+def test_attn_mass_refuses_a_workspace_over_its_operands(ic):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    L, d = 2048, 128
+    n = ic.attn_mass_workspace_bytes(1, L, L, 16, 1, d)
+    assert n > 0 and n % 16 == 0
+    arena = torch.zeros(n + L * 4, device="cuda", dtype=torch.uint8)
+    q, k = (torch.randn(1, L, h, d, device="cuda", generator=g).bfloat16() for h in (16, 1))
+    lse = torch.full((1, L, 16), 8.0, device="cuda")
+    want = ic.attn_mass(q, k, lse, torch.zeros(1, L, device="cuda"))
+    mass = arena[n:].view(torch.float32).view(1, L)
+    ic.attn_mass(q, k, lse, mass, ws=arena)                         # only the bytes needed count
+    torch.cuda.synchronize()
+    assert torch.equal(mass, want) and ic.get_last_device_error() == 0
+    with pytest.raises(ic.IndexCacheError, match="ws overlaps mass"):
+        ic.attn_mass(q, k, lse, arena[n - 4:-4].view(torch.float32).view(1, L), ws=arena)
