@@ -432,8 +432,11 @@ size_t ic_attn_mass_workspace_bytes(int B, int Lq, int Lk, int Hq, int Hkv, int 
  * With Lq > 1 several rows add to one position: their weights are summed as
  * 64-bit fixed point in ws (ic_attn_mass_sparse_workspace_bytes(...) bytes,
  * cleared by the call), whose result does not depend on the order, so the same
- * call gives the same bits.  A sum with a weight that is NaN or above 2 Hq
- * (lse not the row's) comes out NaN.
+ * call gives the same bits.  Each weight (the sum over its heads) is rounded to
+ * a multiple of a power of two that is at most 2^-58 Hq max(Lq, 8 x the number of SMs):
+ * 2^-41 for 8192 rows of 16 heads.  A sum with a weight that is NaN or above 2 Hq
+ * (lse not the row's) comes out NaN; so may the sums of a row whose weights
+ * together pass 2 Hq.  With Lq == 1 the weights are added in fp32.
  */
 int ic_attn_mass_sparse(const uint16_t *q, const uint16_t *k, const int32_t *idx, const float *lse,
                         int B, int Lq, int Lk, int Hq, int Hkv, int d, int k_slots, int q_offset,

@@ -399,6 +399,12 @@ struct SparseMassArgs {
 // One weight's sum over the heads as fixed point; the top bit marks a sum
 // that is not a number (or past every valid one).
 constexpr unsigned long long MASS_NAN = 1ull << 63;
+// What a warp has added of one row counts in units of 2^-20, rounded up.  With
+// the row's own lse its weights sum to at most Hq, repeats included; a warp that
+// passes 2 Hq marks its slots from there on.  So a sum holds at most rows x warps a
+// row x 2 Hq, and the fixed point needs no room for every slot of a row
+// naming one position (8192 rows, 2048 slots, 16 heads: unit 2^-42, not 2^-33).
+constexpr float MASS_ROW_ONE = 1048576.0f;
 
 // A warp takes 32 slots of one row at a time: S = Q K^T by m16n8k16 (heads x
 // slots), four tiles of 8 slots, with the K rows read from global memory
@@ -439,6 +445,8 @@ attn_mass_sparse_kernel(const SparseMassArgs a) {
     const float l0 = __ldg(a.lse + row * a.Hq + g), l1 = two ? __ldg(a.lse + row * a.Hq + g + 8) : -INFINITY;
     const float n0 = -l0 * LOG2E, n1 = -l1 * LOG2E;
     const __nv_bfloat16* kb = a.k + b * a.Lk * D + c * 8;
+    const uint32_t row_most = (uint32_t)(2 * a.Hq) << 20;
+    uint32_t row_sum = 0;                                       // of this warp, at most row_most + 32 * row_most
     for (; s0 < a.slots; s0 += stride) {
         if (id != -1 && (id < 0 || id > t)) {
             report(DEV_ERR_BAD_INDEX);
@@ -485,13 +493,20 @@ attn_mass_sparse_kernel(const SparseMassArgs a) {
                 w[x] = (up ? w[x + h] : w[x]) + got;
             }
         }
-        if (mine < 0 || mine > t) continue;
-        if (a.acc == nullptr)
-            atomicAdd(a.mass + b * a.Lk + mine, w[0]);
-        else if (w[0] >= 0.0f && w[0] <= 2.0f * a.Hq)
-            atomicAdd(a.acc + b * a.Lk + mine, __float2ull_rn(w[0] * a.fixed_one));
-        else
-            atomicOr(a.acc + b * a.Lk + mine, MASS_NAN);
+        const bool named = mine >= 0 && mine <= t;
+        if (a.acc == nullptr) {
+            if (named) atomicAdd(a.mass + b * a.Lk + mine, w[0]);
+            continue;
+        }
+        const bool valid = w[0] >= 0.0f && w[0] <= 2.0f * a.Hq;
+        if (row_sum <= row_most)
+            row_sum += __reduce_add_sync(0xffffffffu, named && valid ? __float2uint_ru(w[0] * MASS_ROW_ONE) : 0u);
+        if (named) {
+            if (valid && row_sum <= row_most)
+                atomicAdd(a.acc + b * a.Lk + mine, __float2ull_rn(w[0] * a.fixed_one));
+            else
+                atomicOr(a.acc + b * a.Lk + mine, MASS_NAN);
+        }
     }
 }
 

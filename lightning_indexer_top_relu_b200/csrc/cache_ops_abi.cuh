@@ -520,19 +520,19 @@ int ic_attn_mass_sparse(const uint16_t* q, const uint16_t* k, const int32_t* idx
     a.mass = mass;
     a.Lq = Lq; a.Lk = Lk; a.Hq = Hq; a.slots = k_slots; a.q_offset = q_offset;
     a.scale_log2 = scale_log2_of(scale, d);
+    // 128 slots a CTA and pass; up to about two waves of CTAs (4 an SM), more
+    // slots a CTA beyond
+    const long long per_row = std::max(1LL, std::min<long long>({(k_slots + 127) / 128, 65535, 8LL * sms / rows}));
     int shift = 0;
     if (need > 0) {
-        // one sum holds at most Lq * k_slots weights of at most 2 Hq: no
+        // one sum holds at most 2 Hq from each warp of each of its rows: no
         // wrap below the mark at bit 63
-        shift = 62 - (int)std::ceil(std::log2(2.0 * Lq * (double)k_slots * Hq));
+        shift = 62 - (int)std::ceil(std::log2(2.0 * Hq * (double)Lq * std::min(4 * per_row, (k_slots + 31LL) / 32)));
         a.fixed_one = std::ldexp(1.0f, shift);
         a.acc = reinterpret_cast<unsigned long long*>(ws);
         cudaError_t e = cudaMemsetAsync(ws, 0, need, st);
         if (e != cudaSuccess) return cuda_fail(e, "attn_mass_sparse workspace clear");
     }
-    // 128 slots a CTA and pass; up to about two waves of CTAs (4 an SM), more
-    // slots a CTA beyond
-    const long long per_row = std::max(1LL, std::min<long long>({(k_slots + 127) / 128, 65535, 8LL * sms / rows}));
     const dim3 grid((unsigned)rows, (unsigned)per_row);
     if (d == 64) ic::attn_mass_sparse_kernel<64><<<grid, 128, 0, st>>>(a);
     else ic::attn_mass_sparse_kernel<128><<<grid, 128, 0, st>>>(a);
