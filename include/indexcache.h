@@ -394,6 +394,15 @@ int ic_prefix_attn(const uint16_t *q, const uint16_t *k_prefix, const uint16_t *
 /* Workspace ic_prefix_attn needs on the current device (0 for invalid sizes). */
 size_t ic_prefix_attn_workspace_bytes(int B, int Lq, int P, int S, int Hq, int Hkv, int d);
 
+/* How ic_prefix_attn runs these sizes on the current device: a sum of the bits
+ * below, -1 for invalid sizes.  A query for tests and measurements; no
+ * device work. */
+#define IC_PREFIX_SHARED 1      /* a CTA has two row tiles, which share its K/V tiles */
+#define IC_PREFIX_FUSED 2       /* CTAs walk over the prefix and then their sequence's own cache */
+#define IC_PREFIX_OWN_KERNEL 4  /* own caches of at most 64 rows in a kernel of their own */
+#define IC_PREFIX_PARTIALS 8    /* a row's keys are split: partial results are merged */
+int ic_prefix_attn_form(int B, int Lq, int P, int S, int Hq, int Hkv, int d);
+
 /*
  * The attention weight each cached position received, added to a running
  * total (what an eviction policy ranks positions by):

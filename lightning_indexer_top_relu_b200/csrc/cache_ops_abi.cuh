@@ -240,6 +240,18 @@ PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int 
     return g;
 }
 
+// The same on the current device (148 SMs without one); false for sizes that
+// are refused.
+bool prefix_geom_of(int B, int Lq, int P, int S, int Hq, int Hkv, int d, PrefixGeom* g) {
+    if (B <= 0 || Lq <= 0 || P < 0 || S < 0 || check_cache_heads(Hq, Hkv, d) ||
+        check_prefix_sizes(B, Lq, P, S, Hq))
+        return false;
+    int dev, sms;
+    if (device_setup(&dev, &sms)) sms = 148;
+    *g = prefix_geom(B, Lq, P, S, Hq, Hkv, d, sms);
+    return true;
+}
+
 // A bf16 tensor map of `rank` dimensions, 128-byte swizzled boxes of 64
 // columns; what lies outside reads as zeros.
 int make_tmap(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
@@ -317,12 +329,15 @@ int launch_prefix_own(const PrefixGeom& g, const ic::PrefixAttnArgs& p, const ui
 extern "C" {
 
 size_t ic_prefix_attn_workspace_bytes(int B, int Lq, int P, int S, int Hq, int Hkv, int d) {
-    if (B <= 0 || Lq <= 0 || P < 0 || S < 0 || check_cache_heads(Hq, Hkv, d) ||
-        check_prefix_sizes(B, Lq, P, S, Hq))
-        return 0;
-    int dev, sms;
-    if (device_setup(&dev, &sms)) sms = 148;
-    return prefix_geom(B, Lq, P, S, Hq, Hkv, d, sms).ws_bytes;
+    PrefixGeom g;
+    return prefix_geom_of(B, Lq, P, S, Hq, Hkv, d, &g) ? g.ws_bytes : 0;
+}
+
+int ic_prefix_attn_form(int B, int Lq, int P, int S, int Hq, int Hkv, int d) {
+    PrefixGeom g;
+    if (!prefix_geom_of(B, Lq, P, S, Hq, Hkv, d, &g)) return -1;
+    return (g.shared ? IC_PREFIX_SHARED : 0) | (g.fused ? IC_PREFIX_FUSED : 0) |
+           (g.own_kernel ? IC_PREFIX_OWN_KERNEL : 0) | (g.slots > 1 ? IC_PREFIX_PARTIALS : 0);
 }
 
 int ic_prefix_attn(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* v_prefix,

@@ -39,7 +39,7 @@ EXPORTS = ("ic_status_string", "ic_last_error_message", "ic_get_last_device_erro
            "ic_sparse_attn_unique_workspace_bytes", "ic_index_overlap",
            "ic_layer_stack_dense_rows", "ic_layer_stack_forward_opts",
            "ic_layer_stack_fused_fallback_blocks", "ic_prefix_attn",
-           "ic_prefix_attn_workspace_bytes", "ic_attn_mass",
+           "ic_prefix_attn_workspace_bytes", "ic_prefix_attn_form", "ic_attn_mass",
            "ic_attn_mass_workspace_bytes", "ic_attn_mass_sparse",
            "ic_attn_mass_sparse_workspace_bytes", "ic_evict_select", "ic_cache_gather")
 
@@ -136,6 +136,8 @@ _lib.ic_prefix_attn.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, 
                                 _Z, _P]
 _lib.ic_prefix_attn_workspace_bytes.restype = _Z
 _lib.ic_prefix_attn_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I, _I]
+_lib.ic_prefix_attn_form.restype = _I
+_lib.ic_prefix_attn_form.argtypes = [_I, _I, _I, _I, _I, _I, _I]
 _lib.ic_attn_mass.restype = _I
 _lib.ic_attn_mass.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _Z, _P]
 _lib.ic_attn_mass_workspace_bytes.restype = _Z
@@ -424,6 +426,16 @@ def _own_shapes(q, k, name="k"):
 
 def prefix_attn_workspace_bytes(B: int, Lq: int, P: int, S: int, Hq: int, Hkv: int, d: int) -> int:
     return int(_lib.ic_prefix_attn_workspace_bytes(B, Lq, P, S, Hq, Hkv, d))
+
+
+# IC_PREFIX_*
+PREFIX_SHARED, PREFIX_FUSED, PREFIX_OWN_KERNEL, PREFIX_PARTIALS = 1, 2, 4, 8
+
+
+def prefix_attn_form(B: int, Lq: int, P: int, S: int, Hq: int, Hkv: int, d: int) -> int:
+    """How prefix_attn runs these sizes on the current device: a sum of
+    PREFIX_* bits (-1: refused)."""
+    return int(_lib.ic_prefix_attn_form(B, Lq, P, S, Hq, Hkv, d))
 
 
 def prefix_attn(q, k_prefix, v_prefix, k=None, v=None, lens=None, scale: float = 0.0, out=None,
