@@ -125,3 +125,42 @@ def test_prefix_attn_forms_against_fp64(ic, case):
         check_attn(out[b], lse[b], q[b], keys, vals, seen)
         check_norm(out[b], q[b], keys, vals, seen)
     assert not torch.isnan(out).any() and not torch.isnan(lse).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sign", [1.0, -1.0], ids=["growing", "falling"])
+@pytest.mark.parametrize("case", [(142, 6, 1822, 0, 8, 2, 64), (30, 9, 3443, 26, 16, 1, 64),
+                                  (282, 5, 1000, 300, 16, 2, 128), (64, 9, 1000, 100, 32, 2, 128),
+                                  (43, 17, 170, 1736, 8, 1, 128), (70, 85, 300, 300, 4, 1, 64),
+                                  (24, 5, 515, 777, 16, 2, 128), (2, 5, 814, 3490, 16, 1, 128),
+                                  (2, 5, 300, 400, 13, 1, 64)], ids=str)
+def test_prefix_attn_forms_move_the_maximum(ic, case, sign):
+    """Scores that grow by 25 a tile of 128 keys along the prefix and again
+    along the own caches: every tile raises the running maximum (falling: none
+    after the first).  Scores reach |z| = 336, whose fp32 value is off by a step
+    of 2^-23 |z| for each of the up to 8 matrix instructions that add to it and
+    two more: 10 * 2^-23 * 336 < 2^-11 of p, that much more of sum p |v| than in the
+    other tests."""
+    B, Lq, P, S, Hq, Hkv, d = case
+    g = gen(sum(case) + 2)
+    q, (kp, k) = randn(g, B, Lq, Hq, d), (randn(g, P, Hkv, d), randn(g, B, S, Hkv, d))
+    vp, v = randn(g, P, Hkv, d).bfloat16(), randn(g, B, S, Hkv, d).bfloat16()
+    q[..., 0] = 8
+
+    def ramp(n):
+        return sign * (torch.arange(n, device="cuda") - n / 2) * (25 / 128) * d ** 0.5 / 8
+    kp[..., 0], k[..., 0] = ramp(P)[:, None], ramp(S)[:, None]
+    q, kp, k = q.bfloat16(), kp.bfloat16(), k.bfloat16()
+    lens = torch.randint(0, S + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    lens[0], lens[1] = S, 0
+    out, lse = ic.prefix_attn(q, kp, vp, *((k, v, lens) if S else ()))
+    ok(ic)
+    at, i = torch.arange(S, device="cuda"), torch.arange(Lq, device="cuda")
+    for b in sorted({0, 1, B // 2, B - 1}):
+        n = int(lens[b])
+        seen = torch.cat([torch.ones(Lq, P, dtype=torch.bool, device="cuda"),
+                          (at[None] <= n - Lq + i[:, None]) & (at[None] < n)], 1)
+        ref, rl, mag, zmax = ref_attn(q[b], torch.cat([kp, k[b]]), torch.cat([vp, v[b]]), seen)
+        err = (out[b].double() - ref).abs()
+        assert (err <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -11) * mag + 1e-30).all()
+        assert (lse[b].double() - rl).abs().max().item() <= 2e-5 * (1 + zmax)
