@@ -15,10 +15,12 @@
 //   adds up the lower slices' keys above the bin, so after the last pass a CTA
 //   knows how many positions the slices before it keep.  A counting pass gives
 //   each warp its share, and the warps write their positions at ballot-prefix
-//   offsets: the output is sorted without a sort.  Bound by the latency of
-//   its barriers and scans (five cluster barriers), not by its one read of
-//   the weights.  (Three passes of 11 + 11 + 10 bits: two 500K caches took 51
-//   us, most of it reading 2048 bins of 16 slices in every CTA.)
+//   offsets: the output is sorted without a sort.  Short slices are bound by the
+//   latency of the barriers and scans (five cluster barriers), long ones by
+//   issue in the five passes over their keys in shared memory (two 500K caches:
+//   32 CTAs at 62%), neither by the one read of the weights.  (Three passes of
+//   11 + 11 + 10 bits: two 500K caches took 51 us, most of it reading 2048 bins
+//   of 16 slices in every CTA.)
 //
 // Compaction (cache_gather_kernel): copies row keep[b, j] of every tensor to
 // row j.  Bound by memory bandwidth.
@@ -115,11 +117,12 @@ evict_select_kernel(const EvictArgs a) {
     uint32_t* keys = reinterpret_cast<uint32_t*>(ev_smem + S::OFF_KEYS);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x, C = gridDim.x, b = blockIdx.y;      // the cluster is one row of the grid
-    // new_lens may be lens, so the length is a plain load, once a thread, and
-    // the new one is written where no thread of the cluster can take it for
-    // the old: here when every position stays (the clamped length itself,
-    // which clamps to the same n), else behind the barriers of the passes
-    const int n = a.lens ? clamp_len(*(const volatile int32_t*)(a.lens + b), a.Lk) : a.Lk;
+    // new_lens may be lens: the length is a plain load, and the new one is
+    // written where no thread of the cluster can take it for the old -- here when
+    // every position stays (the clamped length itself, which clamps to the same
+    // n), else behind the barriers of the passes, which every thread reaches
+    // with its n
+    const int n = a.lens ? clamp_len(a.lens[b], a.Lk) : a.Lk;
     int32_t* keep = a.keep + (long long)b * a.n_keep;
     if (n <= a.n_keep) {                                             // uniform over the cluster
         if (rank == 0 && tid == 0 && a.new_lens) a.new_lens[b] = n;
@@ -199,7 +202,6 @@ evict_select_kernel(const EvictArgs a) {
         }
         __syncthreads();
     }
-    if (rank == 0 && tid == 0 && a.new_lens) a.new_lens[b] = a.n_keep;
     const uint32_t T = kk > 0 ? prefix : 0xffffffffu;    // no weight's key is 0xffffffff
     const int need = remaining;                          // keys equal to T kept, lowest positions first
 
@@ -240,6 +242,7 @@ evict_select_kernel(const EvictArgs a) {
             eq_before += (uint32_t)__popc(me);
         }
     }
+    if (rank == C - 1 && tid == NT - 1 && a.new_lens) a.new_lens[b] = a.n_keep;
     if (C > 1) cluster_sync();               // no CTA leaves while another may read its shared memory
 }
 
