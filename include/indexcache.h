@@ -416,8 +416,9 @@ int ic_prefix_attn_form(int B, int Lq, int P, int S, int Hq, int Hkv, int d);
  * (q_offset + Lq may exceed Lk here: q_offset >= Lk lets every row see every
  * key, as the rows of a batch see a shared prefix).  Rows with
  * lse = -INFINITY add nothing.  Positions that no row sees keep their value,
- * and their keys may hold anything.  Heads and d as in ic_prefix_attn; B <=
- * 65535, Lk <= 2^30, Lq <= 2^29.  The sum has a fixed order: the same call gives
+ * and their keys may hold anything; the sum of a key that some row sees and that
+ * is not finite may be NaN.  Heads and d as in ic_prefix_attn; B <= 65535,
+ * Lk <= 2^30, Lq <= 2^29.  The sum has a fixed order: the same call gives
  * the same bits.
  * ws/ws_bytes: device workspace of ic_attn_mass_workspace_bytes(...) bytes for
  * the sums of rows that several CTAs share (may be NULL when that is 0); less
@@ -436,7 +437,9 @@ size_t ic_attn_mass_workspace_bytes(int B, int Lq, int Lk, int Hq, int Hkv, int 
  * [B, Lq, k_slots] adds its weight to the position it names (a position
  * repeated in a row counts every time, as in ic_sparse_attn, whose lse this
  * takes).  Slots holding -1 are empty; a slot outside [0, t] is skipped and
- * flags IC_ERR_INVALID_ARG in the device error word.  Shapes as in
+ * flags IC_ERR_INVALID_ARG in the device error word.  t = q_offset + i for the
+ * whole batch, as in ic_sparse_attn: there are no lengths by sequence, and a slot
+ * past a sequence's length but not past t counts as a position.  Shapes as in
  * ic_sparse_attn (Hkv == 1, Hq 8 or 16).
  * With Lq > 1 several rows add to one position: their weights are summed as
  * 64-bit fixed point in ws (ic_attn_mass_sparse_workspace_bytes(...) bytes,
