@@ -371,7 +371,8 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     }
 }
 
-// mass += the ranks' sums, in rank order.
+// mass += the ranks' sums, in rank order: at most 32 of them, each compensated
+// over its row tiles, so plain fp32 adds (31 * 2^-24 of the sum at most).
 __global__ void attn_mass_add_kernel(const AttnMassArgs a, int ranks) {
     asm volatile("griddepcontrol.wait;" ::: "memory");          // launched as the sums' dependent
     const int b = blockIdx.y;

@@ -74,7 +74,8 @@ MassGeom mass_geom(int B, int Lq, int Lk, int Hq, int Hkv, int d, int sms) {
     const long long slots = 2LL * sms;                             // CTAs at once
     // few key tiles: several CTAs share one, with at least 8 steps each, as long as
     // they fill the GPU four times; with at least 4 as long as all of them run
-    // at once (200 rows, two K/V heads, 3000 keys: 14 us instead of 32)
+    // at once (200 rows, two K/V heads, 3000 keys: 14 us instead of 32; a few
+    // shapes lose a little: 64 rows of one head, 10000 keys 14.2 instead of 13.4)
     const long long deep = std::min<long long>({g.row_tiles / 8, steps / 8, 4 * slots / tiles});
     const long long wide = std::min<long long>({(long long)g.row_tiles, steps / 4, slots / tiles});
     g.ranks = (int)std::max(1LL, std::min(32LL, std::max(deep, wide)));
@@ -140,9 +141,10 @@ struct PrefixGeom {
 // steps.  Units up to the number of SMs run at once, more run in turn, the last
 // half a unit late on average.  The own-cache kernel reads 40 GB/s an SM (caches
 // taken as three quarters full), on SMs without a unit first.
-//   32 sequences, 32K prefix, caches of 2K: 104 split units of 10 steps 26.6 us,
-//   148 of 7 steps 31.1, 104 shared ones of 10 steps 28.3; without own caches
-//   128 split units of 8 steps 22.7, 148 of 7 steps 24.5.
+//   32 sequences, 32K prefix, caches of 2K: 104 split units of 10 steps measured
+//   26.6 us, 96 of 11 steps, which the estimate takes, 27.4; 148 of 7 steps 31.1,
+//   104 shared ones of 10 steps 28.3; without own caches 128 split units of 8
+//   steps 22.7, 148 of 7 steps 24.5.
 PrefixGeom prefix_geom(int B, int Lq, int P, int S, int Hq, int Hkv, int d, int sms) {
     PrefixGeom g;
     const int T = ic::PA_KEYS, R = ic::PA_ROWS, G = Hq / Hkv;
